@@ -18,7 +18,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcnhwc.so")
 
 OK, INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, MISALIGNED, HIP_ERROR = range(6)
-F16, BF16 = 0, 1
+F16, BF16, F32 = 0, 1, 2
+ACTS = {"silu": 0, "gelu": 1, "relu": 2, "sigmoid": 3}   # CNHWC_ACT_*
 OP_FWD, OP_DGRAD, OP_WGRAD = 1, 2, 4
 (VAR_AUTO, VAR_DGRAD_POINTWISE, VAR_DGRAD_IGEMM, VAR_DGRAD_DW_STREAM, VAR_DGRAD_DW_ROTATED,
  VAR_FWD_DIRECT, VAR_FWD_SPLITC, VAR_FWD_GROUPED, VAR_FWD_GENERIC, VAR_DGRAD_GENERIC,
@@ -27,7 +28,10 @@ OP_FWD, OP_DGRAD, OP_WGRAD = 1, 2, 4
 
 SYMBOLS = ("cnhwc_out_dims", "cnhwc_workspace_size", "cnhwc_plan", "cnhwc_chunk_plan",
            "cnhwc_fwd", "cnhwc_dgrad", "cnhwc_wgrad", "cnhwc_last_error", "cnhwc_set_override",
-           "cnhwc_fwd_static_ws")
+           "cnhwc_fwd_static_ws",
+           "cnhwc_layernorm_fwd", "cnhwc_layernorm_bwd", "cnhwc_layernorm_workspace_size",
+           "cnhwc_gated_fwd", "cnhwc_gated_bwd", "cnhwc_gated_workspace_size", "cnhwc_gated_plan",
+           "cnhwc_dropout")
 STATIC_WS_BYTES = 32 << 20   # CNHWC_STATIC_WS_BYTES
 
 
@@ -49,6 +53,25 @@ class Problem(ctypes.Structure):
 class Override(ctypes.Structure):
     _fields_ = [("variant", ctypes.c_int32), ("cpl", ctypes.c_int32), ("split_c", ctypes.c_int32),
                 ("tune", ctypes.c_int32), ("chunk_limit_bytes", ctypes.c_int64)]
+
+
+class LayernormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("c", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GatedProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("c", ctypes.c_int64), ("f", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class DropoutProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("c", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("p", ctypes.c_double),
+                ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -83,6 +106,16 @@ def lib():
         L.cnhwc_last_error.argtypes = []
         L.cnhwc_last_error.restype = ctypes.c_char_p
         L.cnhwc_set_override.argtypes = [ctypes.POINTER(Override)]
+        LN, GP, DP = (ctypes.POINTER(t) for t in (LayernormProblem, GatedProblem, DropoutProblem))
+        szp = ctypes.POINTER(sz)
+        L.cnhwc_layernorm_fwd.argtypes = [LN, vp, vp, vp, vp, vp, vp, vp]
+        L.cnhwc_layernorm_workspace_size.argtypes = [LN, szp]
+        L.cnhwc_layernorm_bwd.argtypes = [LN, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.cnhwc_gated_workspace_size.argtypes = [GP, ctypes.c_int, ctypes.c_int, szp]
+        L.cnhwc_gated_plan.argtypes = [GP, ctypes.c_int, ctypes.c_char_p, sz]
+        L.cnhwc_gated_fwd.argtypes = [GP, vp, vp, vp, vp, vp, sz, vp]
+        L.cnhwc_gated_bwd.argtypes = [GP, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.cnhwc_dropout.argtypes = [DP, vp, vp, vp, vp, vp]
         for fn in SYMBOLS:
             if fn != "cnhwc_last_error":
                 getattr(L, fn).restype = ctypes.c_int
@@ -226,3 +259,302 @@ def wgrad(x, dy, p, dw=None, ws=None):
                 ws.numel() * ws.element_size() if ws is not None else 0,
                 _stream_handle(torch, x.device))
     return dw
+
+
+# ---- channel mixing: layer norm, gated feed-forward, dropout -------------------
+#
+# x is a device tensor [..., c] whose last dimension is contiguous and whose
+# leading dimensions step evenly (a dense tensor or a channel slice of one), so
+# that it is rows of c channels with one row stride.  Outputs are new dense
+# tensors of x's leading shape unless given.  Work goes to the current stream of
+# x's device; a tensor written on another stream has to be waited for first, as
+# in PyTorch.
+
+def _mix_dtype(torch, t, what, f32=True):
+    kinds = {torch.float16: F16, torch.bfloat16: BF16}
+    if f32:
+        kinds[torch.float32] = F32
+    if t.dtype not in kinds:
+        raise ValueError("%s must be %s (got %s)" % (
+            what, ", ".join(str(k) for k in kinds), t.dtype))
+    return kinds[t.dtype]
+
+
+def _rows(t, what, width=None):
+    """(rows, width, row stride) of a tensor seen as rows of its last dimension."""
+    if t.dim() < 1:
+        raise ValueError("%s needs at least one dimension" % what)
+    c = t.shape[-1]
+    if width is not None and c != width:
+        raise ValueError("%s has %d channels, expected %d" % (what, c, width))
+    rows = 1
+    for s in t.shape[:-1]:
+        rows *= s
+    if rows == 0 or c == 0:
+        return rows, c, c
+    if t.stride(-1) != 1 and c > 1:
+        raise ValueError("%s: channels are not contiguous" % what)
+    stride, inner = None, 1      # walk outwards; dimensions of size 1 have no step
+    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * inner:
+            raise ValueError("%s: its leading dimensions do not step evenly (shape %s, strides %s)"
+                             % (what, tuple(t.shape), tuple(t.stride())))
+        inner *= size
+    if stride is None:
+        stride = c
+    if stride < c:
+        raise ValueError("%s: rows overlap (stride %d, %d channels)" % (what, stride, c))
+    return rows, c, stride
+
+
+def _same(t, ref, what, dtype=None):
+    if t.device != ref.device:
+        raise ValueError("%s is on %s, expected %s" % (what, t.device, ref.device))
+    if t.dtype != (dtype or ref.dtype):
+        raise ValueError("%s is %s, expected %s" % (what, t.dtype, dtype or ref.dtype))
+
+
+def _on_gpu(t, what):
+    if t.device.type != "cuda":
+        raise ValueError("%s must be a GPU tensor (got %s)" % (what, t.device))
+
+
+def _like_rows(t, shape, what, rows, width, ref, dtype=None):
+    """Row stride of an output given by the caller, or a new dense one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype or ref.dtype, device=ref.device), width
+    _same(t, ref, what, dtype)
+    r, _, st = _rows(t, what, width)
+    if r != rows:
+        raise ValueError("%s has %d rows, expected %d" % (what, r, rows))
+    return t, st
+
+
+def _vector(t, n, what, ref, dtype):
+    if t is None:
+        return None
+    _same(t, ref, what, dtype)
+    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous [%d] tensor (got %s)" % (what, n, tuple(t.shape)))
+    return t
+
+
+def _ptr(t):
+    return None if t is None or t.numel() == 0 else t.data_ptr()
+
+
+def _ws(torch, ws, need, device):
+    """(tensor to keep alive, pointer, bytes) of a workspace of `need` bytes."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on %s" % device)
+    return ws, _ptr(ws), ws.numel() * ws.element_size()
+
+
+def _ln_problem(torch, x, gamma, beta, eps, c, rows, xs, ys):
+    dt = _mix_dtype(torch, x, "x")
+    pd = dt
+    for t, what in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            pd = _mix_dtype(torch, t, what)
+            _vector(t, c, what, x, t.dtype)
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise ValueError("gamma is %s and beta is %s" % (gamma.dtype, beta.dtype))
+    return LayernormProblem(rows, c, xs, ys, eps, dt, pd, 0)
+
+
+def layernorm(x, gamma=None, beta=None, eps=1e-5, y=None):
+    """(y, mean, rstd): layer norm of x [..., c] over its channels, and each
+    row's fp32 statistics for layernorm_bwd."""
+    import torch
+    _on_gpu(x, "x")
+    rows, c, xs = _rows(x, "x")
+    y, ys = _like_rows(y, x.shape, "y", rows, c, x)
+    prob = _ln_problem(torch, x, gamma, beta, eps, c, rows, xs, ys)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    with torch.cuda.device(x.device):
+        _check(lib().cnhwc_layernorm_fwd(ctypes.byref(prob), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y),
+                                         _ptr(mean), _ptr(rstd), _stream_handle(torch, x.device)))
+    return y, mean, rstd
+
+
+def layernorm_workspace(x, gamma=None):
+    """Workspace bytes of layernorm_bwd for this x."""
+    import torch
+    rows, c, xs = _rows(x, "x")
+    b = ctypes.c_size_t()
+    prob = _ln_problem(torch, x, gamma, None, 0.0, c, rows, xs, 0)
+    _check(lib().cnhwc_layernorm_workspace_size(ctypes.byref(prob), ctypes.byref(b)))
+    return b.value
+
+
+def layernorm_bwd(dy, x, mean, rstd, gamma=None, dx=None, param_dtype=None, ws=None):
+    """(dx, dgamma, dbeta) of layernorm, from its x and statistics.  dgamma and
+    dbeta have gamma's type (param_dtype, or x's, without a gamma).  dx, if
+    given, has x's row stride."""
+    import torch
+    _on_gpu(x, "x")
+    rows, c, xs = _rows(x, "x")
+    _same(dy, x, "dy")
+    drows, _, ys = _rows(dy, "dy", c)
+    if drows != rows:
+        raise ValueError("dy has %d rows, x has %d" % (drows, rows))
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        _same(t, x, what, torch.float32)
+        if t.numel() != rows or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous tensor of %d values" % (what, rows))
+    prob = _ln_problem(torch, x, gamma, None, 0.0, c, rows, xs, ys)
+    pd = gamma.dtype if gamma is not None else (param_dtype or x.dtype)
+    if param_dtype is not None and param_dtype != pd:
+        raise ValueError("param_dtype is %s, gamma is %s" % (param_dtype, pd))
+    prob.param_dtype = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(pd, -1)
+    if dx is None:
+        dx = _new_rows(torch, x.shape, xs, x)
+    else:
+        _same(dx, x, "dx")
+        if _rows(dx, "dx", c)[::2] != (rows, xs):
+            raise ValueError("dx must have x's rows and row stride (%d)" % xs)
+    dgamma = torch.empty(c, dtype=pd, device=x.device)
+    dbeta = torch.empty_like(dgamma)
+    need = ctypes.c_size_t()
+    _check(lib().cnhwc_layernorm_workspace_size(ctypes.byref(prob), ctypes.byref(need)))
+    ws, wp, wb = _ws(torch, ws, need.value, x.device)
+    with torch.cuda.device(x.device):
+        _check(lib().cnhwc_layernorm_bwd(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                         _ptr(dx), _ptr(dgamma), _ptr(dbeta), wp, wb,
+                                         _stream_handle(torch, x.device)))
+    return dx, dgamma, dbeta
+
+
+def _new_rows(torch, shape, stride, ref):
+    """A new tensor of `shape` with the given row stride (the entry points give
+    dx the row stride of x)."""
+    c = shape[-1]
+    rows = 1
+    for s in shape[:-1]:
+        rows *= s
+    if stride == c or rows == 0:
+        return torch.empty(shape, dtype=ref.dtype, device=ref.device)
+    return torch.empty((*shape[:-1], stride), dtype=ref.dtype, device=ref.device)[..., :c]
+
+
+def _gated_problem(torch, x, wg, wu, act, ys=0):
+    _on_gpu(x, "x")
+    rows, c, xs = _rows(x, "x")
+    dt = _mix_dtype(torch, x, "x", f32=False)
+    if act not in ACTS:
+        raise ValueError("act must be one of %s (got %r)" % (", ".join(ACTS), act))
+    f = wg.shape[0]
+    for w, what in ((wg, "wg"), (wu, "wu")):
+        _same(w, x, what)
+        # [f, c], or the [f, 1, 1, c] filter of a pointwise convolution
+        if w.dim() < 2 or w.shape[0] != f or w.shape[-1] != c or w.numel() != f * c or not w.is_contiguous():
+            raise ValueError("%s must be a contiguous [%d, %d] tensor (got %s)" % (what, f, c, tuple(w.shape)))
+    return GatedProblem(rows, c, f, xs, ys, ACTS[act], dt, 0)
+
+
+def _gated_need(prob, op, unaligned):
+    b = ctypes.c_size_t()
+    _check(lib().cnhwc_gated_workspace_size(ctypes.byref(prob), op, int(unaligned), ctypes.byref(b)))
+    return b.value
+
+
+def _off16(*tensors):
+    return any(t.data_ptr() % 16 for t in tensors)
+
+
+def gated_workspace(x, wg, which="fwd"):
+    """Workspace bytes of gated (which="fwd") or gated_bwd ("bwd") for operands
+    like x and wg."""
+    import torch
+    if which not in ("fwd", "bwd"):
+        raise ValueError('which must be "fwd" or "bwd" (got %r)' % (which,))
+    prob = _gated_problem(torch, x, wg, wg, "silu")
+    return _gated_need(prob, OP_FWD if which == "fwd" else OP_DGRAD, _off16(x, wg))
+
+
+def gated_plan(x, wg, which="fwd"):
+    """Names of the kernels the call runs on 16-byte-aligned operands."""
+    import torch
+    prob = _gated_problem(torch, x, wg, wg, "silu")
+    buf = ctypes.create_string_buffer(256)
+    _check(lib().cnhwc_gated_plan(ctypes.byref(prob), OP_FWD if which == "fwd" else OP_DGRAD, buf, 256))
+    return buf.value.decode()
+
+
+def gated(x, wg, wu, act="silu", y=None, ws=None):
+    """act(x wg^T) * (x wu^T) of x [..., c] and wg, wu [f, c] (or [f, 1, 1, c])."""
+    import torch
+    prob = _gated_problem(torch, x, wg, wu, act)
+    y, prob.y_stride = _like_rows(y, (*x.shape[:-1], prob.f), "y", prob.rows, prob.f, x)
+    need = _gated_need(prob, OP_FWD, _off16(x, wg, wu))
+    ws, wp, wb = _ws(torch, ws, need, x.device)
+    with torch.cuda.device(x.device):
+        _check(lib().cnhwc_gated_fwd(ctypes.byref(prob), _ptr(x), _ptr(wg), _ptr(wu), _ptr(y), wp, wb,
+                                     _stream_handle(torch, x.device)))
+    return y
+
+
+def gated_bwd(dy, x, wg, wu, act="silu", need_dx=True, need_dw=True, ws=None):
+    """(dx, dwg, dwu) of gated; None in the place of what is not needed.  dx
+    has x's row stride."""
+    import torch
+    prob = _gated_problem(torch, x, wg, wu, act)
+    _same(dy, x, "dy")
+    drows, _, prob.y_stride = _rows(dy, "dy", prob.f)
+    if drows != prob.rows:
+        raise ValueError("dy has %d rows, x has %d" % (drows, prob.rows))
+    dx = _new_rows(torch, x.shape, prob.x_stride, x) if need_dx else None
+    dwg = torch.empty_like(wg) if need_dw else None
+    dwu = torch.empty_like(wu) if need_dw else None
+    need = _gated_need(prob, OP_DGRAD, _off16(x, wg, wu))
+    ws, wp, wb = _ws(torch, ws, need, x.device)
+    with torch.cuda.device(x.device):
+        # an empty x has no dx to ask for
+        _check(lib().cnhwc_gated_bwd(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(dx), _ptr(dwg),
+                                     _ptr(dwu), wp, wb, _stream_handle(torch, x.device))
+               if prob.rows or need_dw else OK)
+    return dx, dwg, dwu
+
+
+def dropout(x, p, seed, offset=0, residual=None, y=None, device_offset=None):
+    """residual + (keep ? x / (1 - p) : 0), the mask drawn by Philox4x32-10 from
+    (seed, offset, element index).  device_offset: an int64 device tensor of one
+    value that is added to offset when the kernel runs."""
+    import torch
+    _on_gpu(x, "x")
+    rows, c, xs = _rows(x, "x")
+    rs = 0
+    if residual is not None:
+        _same(residual, x, "residual")
+        rrows, _, rs = _rows(residual, "residual", c)
+        if rrows != rows:
+            raise ValueError("residual has %d rows, x has %d" % (rrows, rows))
+    if device_offset is not None:
+        _same(device_offset, x, "device_offset", torch.int64)
+        if device_offset.numel() != 1:
+            raise ValueError("device_offset must hold one value")
+    for v, what in ((seed, "seed"), (offset, "offset")):
+        if not 0 <= v < 1 << 64:
+            raise ValueError("%s must be in [0, 2^64) (got %d)" % (what, v))
+    y, ys = _like_rows(y, x.shape, "y", rows, c, x)
+    prob = DropoutProblem(rows, c, xs, rs, ys, p, seed, offset, _mix_dtype(torch, x, "x"), 0)
+    with torch.cuda.device(x.device):
+        _check(lib().cnhwc_dropout(ctypes.byref(prob), _ptr(x), _ptr(residual), _ptr(y), _ptr(device_offset),
+                                   _stream_handle(torch, x.device)))
+    return y
+
+
+def dropout_bwd(dy, p, seed, offset=0, dx=None, device_offset=None):
+    """The gradient of dropout in x (the residual's is dy itself): the same mask
+    drawn again."""
+    return dropout(dy, p, seed, offset, y=dx, device_offset=device_offset)

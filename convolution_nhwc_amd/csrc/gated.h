@@ -1,0 +1,118 @@
+// Internals of the gated feed-forward block (gated_gemm.hip, gated_rows.hip,
+// mix_host.cpp).
+#pragma once
+
+#include "mix.h"
+
+namespace cnhwc {
+
+// The four products of the two passes on the tiled kernel:
+//   PROJ  [g | u] = x [wg ; wu]^T       both operands k-contiguous, g and u of one
+//                                       element in the same lane
+//   DX    dx = [dg | du] [wg ; wu]      right operand rows are the reduction
+//   DW    [dwg ; dwu] = [dg | du]^T x   both operands' rows are the reduction
+enum GatedProduct { kProj = 0, kDx = 1, kDw = 2 };
+
+// What a kernel does with its sums: round them (PROJ: y = act(g) u), form dg
+// and du (PROJ), or store them as partial sums of a split reduction.
+enum GatedEnd { kEndFwd = 0, kEndBwd = 1, kEndPart = 2 };
+
+struct GatedArgs {
+    // operands, rows of ld elements (a multiple of 8), 16-byte aligned
+    const void* a;          // PROJ: x   DX, DW: dg | du [rows][2 fp]
+    const void* b0;         // PROJ, DX: wg   DW: x
+    const void* b1;         // PROJ, DX: wu   DW: unused
+    int64_t lda, ldb;
+    int64_t m;              // output rows: PROJ, DX: rows   DW: 2 fp
+    int64_t n;              // output columns: PROJ: f (of g and of u)   DX, DW: c
+    int64_t k;              // reduction length: PROJ: c   DX: fp (of each half)   DW: rows
+    int64_t nb;             // DX, DW: columns of the right operand's rows (a multiple of 8, >= n)
+    int segs;               // DX: 2 (dg with wg, du with wu), else 1
+    int steps_seg;          // 64-deep steps of one segment
+    int splits;             // reduction splits
+    int act, end;           // PROJ
+    int64_t f, fp;          // hidden width, and rounded up to a multiple of 8
+    // results
+    void* y;                // PROJ forward: y   DX: dx
+    int64_t ldy;
+    const void* dy;         // PROJ backward
+    int64_t lddy;
+    void* dgu;              // PROJ backward: dg | du [rows][2 fp]
+    void* dwg;              // DW [f][c]
+    void* dwu;
+    float* part;            // splits > 1: [splits][m][part_ld] fp32
+    int64_t part_ld;        // PROJ: 2 fp   DX, DW: n rounded up to a multiple of 4
+    int tiles_m, tiles_n;
+};
+
+// The tile shapes: 256 x 256 with one block of 8 waves a CU, 128 x 128 with
+// two blocks of 4 waves a CU.
+constexpr int kGatedBig = 256, kGatedSmall = 128;
+
+int launch_gated_product(int dtype, GatedProduct prod, int tile, const GatedArgs& a, hipStream_t st);
+// Folds the partial sums of a split product into its result.
+int launch_gated_reduce(int dtype, GatedProduct prod, const GatedArgs& a, hipStream_t st);
+// dst [rows][ldd] = src [rows][cols] (row stride lds), columns cols..ldd-1 zero.
+int launch_gated_pack(const void* src, int64_t lds, int64_t rows, int64_t cols, void* dst, int64_t ldd,
+                      hipStream_t st);
+// dst[0..n) = 0 (16-bit elements)
+int launch_gated_zero(void* dst, int64_t n, hipStream_t st);
+
+// Few rows: the weights are streamed once, any strides and alignment.
+constexpr int kGatedFewRows = 64;
+struct GatedRowsArgs {
+    const void* x;
+    const void* wg;
+    const void* wu;
+    void* y;
+    int64_t rows, c, f, ldx, ldy;
+    int act;
+};
+int launch_gated_rows(int dtype, const GatedRowsArgs& a, hipStream_t st);
+
+#ifdef __HIPCC__
+
+// exp and the reciprocal below are the hardware's (1 ulp): their error is far
+// under the rounding of the 16-bit result.
+__device__ inline float sigmoid_f(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+// act(g)
+__device__ inline float act_value(int act, float g) {
+    switch (act) {
+    case CNHWC_ACT_SILU: return g * sigmoid_f(g);
+    case CNHWC_ACT_GELU: return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    case CNHWC_ACT_RELU: return g > 0.0f ? g : (g != g ? g : 0.0f);
+    default: return sigmoid_f(g);
+    }
+}
+
+// act(g) and act'(g)
+__device__ inline void act_both(int act, float g, float& v, float& d) {
+    switch (act) {
+    case CNHWC_ACT_SILU: {
+        const float s = sigmoid_f(g);
+        v = g * s;
+        d = s * (1.0f + g * (1.0f - s));
+        break;
+    }
+    case CNHWC_ACT_GELU: {
+        const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        v = g * c;
+        d = c + g * (__expf(-0.5f * g * g) * 0.39894228040143268f);
+        break;
+    }
+    case CNHWC_ACT_RELU:
+        v = g > 0.0f ? g : (g != g ? g : 0.0f);
+        d = g > 0.0f ? 1.0f : 0.0f;
+        break;
+    default: {
+        const float s = sigmoid_f(g);
+        v = s;
+        d = s * (1.0f - s);
+    }
+    }
+}
+
+#endif
+
+}  // namespace cnhwc

@@ -516,6 +516,8 @@ int run_wgrad(const cnhwc_problem* prob, const void* x, const void* dy, void* dw
 
 int set_error(int status, const std::string& why) { return fail(status, why); }
 
+const cnhwc_override& current_override() { return g_ov; }
+
 }  // namespace cnhwc
 
 using namespace cnhwc;

@@ -121,6 +121,9 @@ int64_t wgrad_split_elems(const Prob& p);
 // Records `why` as this thread's cnhwc_last_error() reason and returns status.
 int set_error(int status, const std::string& why);
 
+// This thread's test override (cnhwc_set_override).
+const cnhwc_override& current_override();
+
 // ---- per-variant acceptance (empty string = accepted, else the reason) ------
 std::string dgrad_igemm_reason(const Prob& p, bool pointwise);
 std::string dw_stream_reason(const Prob& p, int cpl);

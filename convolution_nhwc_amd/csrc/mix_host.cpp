@@ -1,0 +1,605 @@
+// C ABI of the channel-mixing operators: argument checks, workspace sizes, the
+// choice of kernels and the launches.  No device code lives here.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+#include <exception>
+#include <string>
+
+#include "gated.h"
+#include "layernorm.h"
+
+namespace cnhwc {
+namespace {
+
+constexpr int64_t kMaxI32 = 0x7fffffff;
+constexpr int64_t kMaxRowBytes = int64_t(1) << 61;
+
+int fail(int status, const std::string& why) { return set_error(status, why); }
+int ok() { return set_error(CNHWC_OK, ""); }
+int bad(const std::string& why) { return set_error(CNHWC_INVALID_ARG, why); }
+
+// No exception may cross the C boundary (a reason string can fail to allocate).
+template <typename F>
+int guarded(F&& f) {
+    try {
+        return f();
+    } catch (const std::exception&) {
+        return CNHWC_INVALID_ARG;
+    }
+}
+
+int elem_bytes(int dtype) { return dtype == CNHWC_F32 ? 4 : 2; }
+
+std::string num(int64_t v) { return std::to_string(v); }
+
+int check_rows(int64_t rows) {
+    if (rows < 0) return bad("rows must be >= 0 (got " + num(rows) + ")");
+    return CNHWC_OK;
+}
+
+// A row stride: 0 (dense) or at least the row's width; writes the effective one.
+int check_stride(int64_t stride, int64_t width, int64_t rows, int es, const char* what, int64_t* out) {
+    if (stride != 0 && stride < width)
+        return bad(std::string(what) + " must be 0 or >= " + num(width) + " (got " + num(stride) + ")");
+    *out = stride ? stride : width;
+    if (rows > 0 && *out > kMaxRowBytes / es / rows)
+        return bad(std::string(what) + " * rows exceeds the address range");
+    return CNHWC_OK;
+}
+
+struct View {
+    const char* name;
+    const void* p;
+    int64_t bytes;    // first to last byte
+    int align;
+};
+
+View rows_view(const char* name, const void* p, int64_t rows, int64_t stride, int64_t width, int es) {
+    return {name, p, rows > 0 ? ((rows - 1) * stride + width) * es : 0, es};
+}
+
+int check_view(const View& v) {
+    if (v.bytes == 0) return CNHWC_OK;   // nothing of it is read or written
+    if (!v.p) return bad(std::string(v.name) + " is NULL");
+    if (reinterpret_cast<uintptr_t>(v.p) % unsigned(v.align) != 0)
+        return fail(CNHWC_MISALIGNED, std::string(v.name) + " is not " + num(v.align) + "-byte aligned");
+    return CNHWC_OK;
+}
+
+bool overlap(const View& a, const View& b) {
+    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + uintptr_t(b.bytes) && y < x + uintptr_t(a.bytes);
+}
+
+// Every view valid; no written one overlapping any other.
+int check_views(const View* in, int nin, const View* out, int nout) {
+    for (int i = 0; i < nin; ++i)
+        if (int st = check_view(in[i])) return st;
+    for (int i = 0; i < nout; ++i)
+        if (int st = check_view(out[i])) return st;
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (overlap(out[i], in[j])) return bad(std::string(out[i].name) + " overlaps " + in[j].name);
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return bad(std::string(out[i].name) + " overlaps " + out[j].name);
+    }
+    return CNHWC_OK;
+}
+
+int launched(const char* what) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return fail(CNHWC_HIP_ERROR, std::string("launch of ") + what + " failed: " + hipGetErrorString(e));
+    return CNHWC_OK;
+}
+
+// ---- layer norm -----------------------------------------------------------------
+
+struct Ln {
+    int64_t rows, c, xs, ys;
+    float eps;
+    int dtype, param;
+};
+
+int validate(const cnhwc_layernorm_problem* q, Ln* o) {
+    if (!q) return bad("problem descriptor is NULL");
+    if (q->reserved != 0) return bad("reserved field must be 0");
+    if (int st = check_rows(q->rows)) return st;
+    if (q->c < 1 || q->c > kMaxI32) return bad("c must be in [1, 2^31) (got " + num(q->c) + ")");
+    if (!(q->eps >= 0.0f) || !std::isfinite(q->eps)) return bad("eps must be finite and >= 0");
+    if (q->dtype != CNHWC_F16 && q->dtype != CNHWC_BF16 && q->dtype != CNHWC_F32)
+        return bad("dtype must be CNHWC_F16, CNHWC_BF16 or CNHWC_F32 (got " + num(q->dtype) + ")");
+    if (q->param_dtype != q->dtype && q->param_dtype != CNHWC_F32)
+        return bad("param_dtype must be dtype or CNHWC_F32 (got " + num(q->param_dtype) + ")");
+    *o = {q->rows, q->c, 0, 0, q->eps, q->dtype, q->param_dtype};
+    const int es = elem_bytes(q->dtype);
+    if (int st = check_stride(q->x_stride, q->c, q->rows, es, "x_stride", &o->xs)) return st;
+    return check_stride(q->y_stride, q->c, q->rows, es, "y_stride", &o->ys);
+}
+
+LnArgs ln_args(const Ln& p) {
+    LnArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.rows = p.rows;
+    a.x_stride = p.xs;
+    a.y_stride = p.ys;
+    a.c = int(p.c);
+    a.eps = p.eps;
+    a.cf = float(p.c);
+    return a;
+}
+
+int64_t ln_part_bytes(const Ln& p) { return int64_t(layernorm_bwd_blocks(p.dtype, p.rows, p.c)) * 2 * p.c * 4; }
+
+// ---- gated feed-forward ------------------------------------------------------------
+
+struct Gated {
+    int64_t rows, c, f, xs, ys;
+    int act, dtype;
+};
+
+constexpr int64_t kGatedMaxDim = int64_t(1) << 20;
+
+int validate(const cnhwc_gated_problem* q, Gated* o) {
+    if (!q) return bad("problem descriptor is NULL");
+    if (q->reserved != 0) return bad("reserved field must be 0");
+    if (int st = check_rows(q->rows)) return st;
+    if (q->rows > kMaxI32) return bad("rows must be < 2^31");
+    if (q->c < 1 || q->c > kGatedMaxDim) return bad("c must be in [1, 2^20] (got " + num(q->c) + ")");
+    if (q->f < 1 || q->f > kGatedMaxDim) return bad("f must be in [1, 2^20] (got " + num(q->f) + ")");
+    if (q->act < CNHWC_ACT_SILU || q->act > CNHWC_ACT_SIGMOID)
+        return bad("act must be a CNHWC_ACT_* (got " + num(q->act) + ")");
+    if (q->dtype != CNHWC_F16 && q->dtype != CNHWC_BF16)
+        return bad("dtype must be CNHWC_F16 or CNHWC_BF16 (got " + num(q->dtype) + ")");
+    *o = {q->rows, q->c, q->f, 0, 0, q->act, q->dtype};
+    if (int st = check_stride(q->x_stride, q->c, q->rows, 2, "x_stride", &o->xs)) return st;
+    if (int st = check_stride(q->y_stride, q->f, q->rows, 2, "y_stride", &o->ys)) return st;
+    if (o->xs > 2 * kGatedMaxDim) return bad("x_stride must be <= 2^21");
+    if (o->ys > 2 * kGatedMaxDim) return bad("y_stride must be <= 2^21");
+    return CNHWC_OK;
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The tile and the number of reduction splits of one product.
+struct Shape {
+    int tile, splits;
+    int64_t tiles_m, tiles_n;
+};
+
+// Estimated time of each choice in steps of the big tile, the least one wins.
+// One CU runs one big block or two small ones; a round of small blocks does
+// half a big round's work per step in more than half its time, so small tiles
+// win where big ones leave CUs idle.
+Shape choose_shape(int64_t m, int64_t n, int64_t steps, bool dual) {
+    const cnhwc_override& ov = current_override();
+    Shape best = {0, 0, 0, 0};
+    double best_cost = 0;
+    for (int tile : {kGatedBig, kGatedSmall}) {
+        if ((ov.tune == kGatedBig || ov.tune == kGatedSmall) && ov.tune != tile) continue;
+        const int64_t tm = ceil_div(m, tile), tn = ceil_div(n, dual ? tile / 2 : tile);
+        const int64_t slots = tile == kGatedBig ? kNumCUs : 2 * kNumCUs;
+        const double step_cost = tile == kGatedBig ? 1.0 : 0.6;
+        const double fixed = tile == kGatedBig ? 6.0 : 4.0;   // prologue, results
+        // one split per power of two, each at least four steps deep
+        const int64_t forced = std::min<int64_t>(ov.split_c, steps);
+        for (int64_t s = forced > 0 ? forced : 1; s <= 64 && (s == 1 || s == forced || steps / s >= 4);
+             s = forced > 0 ? 65 : s * 2) {
+            const int64_t rounds = ceil_div(tm * tn * s, slots);
+            double cost = double(rounds) * (double(ceil_div(steps, s)) * step_cost + fixed);
+            if (s > 1) {
+                // partial sums written and read at a few TB/s, and one more launch
+                const double bytes = double(tm * tn * s) * tile * tile * 8;
+                cost += 4.0 + bytes / 4.0e6;
+            }
+            if (best.tile == 0 || cost < best_cost) {
+                best = {tile, int(s), tm, tn};
+                best_cost = cost;
+            }
+        }
+    }
+    return best;
+}
+
+int64_t part_bytes(const Shape& s, int64_t m, int64_t ld) { return s.splits > 1 ? s.splits * m * ld * 4 : 0; }
+
+// Everything one pass needs, with the workspace laid out.
+struct GatedPlan {
+    bool few_rows = false;            // forward on the few-rows kernel
+    bool pack_x = false, pack_w = false;
+    int64_t cp, fp;                   // c, f rounded up to multiples of 8
+    Shape proj{}, dx{}, dw{};
+    int64_t off_x = 0, off_wg = 0, off_wu = 0, off_dgu = 0, off_part = 0, bytes = 0;
+};
+
+GatedPlan plan_gated(const Gated& p, int op, bool x_off, bool w_off) {
+    GatedPlan g;
+    g.cp = up(p.c, 8);
+    g.fp = up(p.f, 8);
+    if (p.rows == 0) return g;
+    if (op == CNHWC_OP_FWD && p.rows <= kGatedFewRows) {
+        g.few_rows = true;
+        return g;
+    }
+    // x also where a row gap would put columns past c next to a row's end:
+    // those are masked, so only the 16-byte alignment of every row counts
+    g.pack_x = x_off || p.xs % 8 != 0 || p.c % 8 != 0;
+    g.pack_w = w_off || p.c % 8 != 0;
+    auto take = [&](int64_t n) {
+        const int64_t at = g.bytes;
+        g.bytes = up(at + n, 256);
+        return at;
+    };
+    if (g.pack_x) g.off_x = take(p.rows * g.cp * 2);
+    if (g.pack_w) {
+        g.off_wg = take(p.f * g.cp * 2);
+        g.off_wu = take(p.f * g.cp * 2);
+    }
+    const int64_t csteps = ceil_div(g.cp, 64);
+    g.proj = choose_shape(p.rows, p.f, csteps, true);
+    int64_t part = part_bytes(g.proj, p.rows, 2 * g.fp);
+    if (op != CNHWC_OP_FWD) {
+        g.off_dgu = take(p.rows * 2 * g.fp * 2);
+        g.dx = choose_shape(p.rows, p.c, 2 * ceil_div(g.fp, 64), false);
+        g.dw = choose_shape(2 * g.fp, p.c, ceil_div(p.rows, 64), false);
+        part = std::max(part, std::max(part_bytes(g.dx, p.rows, up(p.c, 4)), part_bytes(g.dw, 2 * g.fp, up(p.c, 4))));
+    }
+    if (part) g.off_part = take(part);
+    return g;
+}
+
+bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
+
+const char* dt_name(int dtype) { return dtype == CNHWC_F16 ? "f16" : "bf16"; }
+
+std::string shape_name(const char* what, int dtype, const Shape& s) {
+    std::string n = std::string("gated_") + what + "_" + dt_name(dtype) + "_t" + num(s.tile);
+    if (s.splits > 1) n += "_split" + num(s.splits) + "+join";
+    return n;
+}
+
+// One product on the tiled kernel, and the join of its splits.
+int run_product(int dtype, GatedProduct prod, const Shape& s, GatedArgs a, char* ws, int64_t off_part,
+                hipStream_t st) {
+    a.tiles_m = int(s.tiles_m);
+    a.tiles_n = int(s.tiles_n);
+    a.splits = s.splits;
+    a.part = s.splits > 1 ? reinterpret_cast<float*>(ws + off_part) : nullptr;
+    if (s.tiles_m * s.tiles_n > kMaxI32 / s.splits)
+        return fail(CNHWC_UNSUPPORTED, "the problem needs more than 2^31 tiles");
+    int rc = launch_gated_product(dtype, prod, s.tile, a, st);
+    if (rc) return fail(rc, "launcher of the gated product refused it");
+    if ((rc = launched("gated_gemm"))) return rc;
+    if (s.splits > 1) {
+        launch_gated_reduce(dtype, prod, a, st);
+        if ((rc = launched("gated_join"))) return rc;
+    }
+    return CNHWC_OK;
+}
+
+int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const void* x, const void* wg, const void* wu,
+              void* y, void* dx, void* dwg, void* dwu, void* ws, size_t ws_bytes, void* stream) {
+    Gated p;
+    int rc = validate(prob, &p);
+    if (rc) return rc;
+    const bool bwd = op != CNHWC_OP_FWD;
+    if (bwd) {
+        if ((dwg == nullptr) != (dwu == nullptr)) return bad("dwg and dwu must both be given or both be NULL");
+        if (!dx && !dwg) return bad("dx, dwg and dwu are all NULL");
+    }
+    View in[4], out[4];
+    int nin = 0, nout = 0;
+    in[nin++] = rows_view("x", x, p.rows, p.xs, p.c, 2);
+    in[nin++] = rows_view("wg", wg, p.f, p.c, p.c, 2);
+    in[nin++] = rows_view("wu", wu, p.f, p.c, p.c, 2);
+    if (bwd) in[nin++] = rows_view("dy", dy, p.rows, p.ys, p.f, 2);
+    if (!bwd) out[nout++] = rows_view("y", y, p.rows, p.ys, p.f, 2);
+    if (dx) out[nout++] = rows_view("dx", dx, p.rows, p.xs, p.c, 2);
+    if (dwg) {
+        out[nout++] = rows_view("dwg", dwg, p.f, p.c, p.c, 2);
+        out[nout++] = rows_view("dwu", dwu, p.f, p.c, p.c, 2);
+    }
+    if ((rc = check_views(in, nin, out, nout))) return rc;
+    const GatedPlan g = plan_gated(p, op, off16(x), off16(wg) || off16(wu));
+    if (g.bytes > 0) {
+        const View wv = {"workspace", ws, g.bytes, 16};
+        if ((rc = check_view(wv))) return rc;
+        if (int64_t(ws_bytes) < g.bytes)
+            return fail(CNHWC_WORKSPACE_TOO_SMALL,
+                        "workspace needs " + num(g.bytes) + " bytes, got " + std::to_string(ws_bytes));
+        for (int i = 0; i < nin; ++i)
+            if (overlap(wv, in[i])) return bad(std::string("workspace overlaps ") + in[i].name);
+        for (int i = 0; i < nout; ++i)
+            if (overlap(wv, out[i])) return bad(std::string("workspace overlaps ") + out[i].name);
+    }
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    (void)hipGetLastError();   // a stale error from earlier work must not be blamed on this call
+    if (p.rows == 0) {
+        if (dwg) {
+            launch_gated_zero(dwg, p.f * p.c, st);   // sums over no rows
+            if ((rc = launched("gated_zero"))) return rc;
+            launch_gated_zero(dwu, p.f * p.c, st);
+            if ((rc = launched("gated_zero"))) return rc;
+        }
+        return ok();
+    }
+    if (g.few_rows) {
+        GatedRowsArgs a = {x, wg, wu, y, p.rows, p.c, p.f, p.xs, p.ys, p.act};
+        launch_gated_rows(p.dtype, a, st);
+        if ((rc = launched("gated_rows"))) return rc;
+        return ok();
+    }
+    char* w = static_cast<char*>(ws);
+    const void *xo = x, *go = wg, *uo = wu;
+    int64_t ldx = p.xs;
+    if (g.pack_x) {
+        launch_gated_pack(x, p.xs, p.rows, p.c, w + g.off_x, g.cp, st);
+        if ((rc = launched("gated_pack"))) return rc;
+        xo = w + g.off_x;
+        ldx = g.cp;
+    }
+    if (g.pack_w) {
+        launch_gated_pack(wg, p.c, p.f, p.c, w + g.off_wg, g.cp, st);
+        if ((rc = launched("gated_pack"))) return rc;
+        launch_gated_pack(wu, p.c, p.f, p.c, w + g.off_wu, g.cp, st);
+        if ((rc = launched("gated_pack"))) return rc;
+        go = w + g.off_wg;
+        uo = w + g.off_wu;
+    }
+    GatedArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.a = xo;
+    a.b0 = go;
+    a.b1 = uo;
+    a.lda = ldx;
+    a.ldb = g.cp;
+    a.m = p.rows;
+    a.n = p.f;
+    a.k = g.cp;
+    a.segs = 1;
+    a.steps_seg = int(ceil_div(g.cp, 64));
+    a.act = p.act;
+    a.end = bwd ? kEndBwd : kEndFwd;
+    a.f = p.f;
+    a.fp = g.fp;
+    a.y = y;
+    a.ldy = p.ys;
+    a.dy = dy;
+    a.lddy = p.ys;
+    a.dgu = bwd ? w + g.off_dgu : nullptr;
+    a.part_ld = 2 * g.fp;
+    if ((rc = run_product(p.dtype, kProj, g.proj, a, w, g.off_part, st))) return rc;
+    if (dx) {
+        GatedArgs d = a;
+        d.a = w + g.off_dgu;
+        d.lda = 2 * g.fp;
+        d.n = p.c;
+        d.k = g.fp;
+        d.nb = g.cp;
+        d.segs = 2;
+        d.steps_seg = int(ceil_div(g.fp, 64));
+        d.y = dx;
+        d.ldy = p.xs;
+        d.part_ld = up(p.c, 4);
+        if ((rc = run_product(p.dtype, kDx, g.dx, d, w, g.off_part, st))) return rc;
+    }
+    if (dwg) {
+        GatedArgs d = a;
+        d.a = w + g.off_dgu;
+        d.lda = 2 * g.fp;
+        d.b0 = xo;
+        d.b1 = nullptr;
+        d.ldb = ldx;
+        d.m = 2 * g.fp;
+        d.n = p.c;
+        d.k = p.rows;
+        d.nb = g.cp;
+        d.steps_seg = int(ceil_div(p.rows, 64));
+        d.dwg = dwg;
+        d.dwu = dwu;
+        d.part_ld = up(p.c, 4);
+        if ((rc = run_product(p.dtype, kDw, g.dw, d, w, g.off_part, st))) return rc;
+    }
+    return ok();
+}
+
+}  // namespace
+}  // namespace cnhwc
+
+using namespace cnhwc;
+
+extern "C" {
+
+int cnhwc_layernorm_fwd(const cnhwc_layernorm_problem* prob, const void* x, const void* gamma, const void* beta,
+                        void* y, float* mean, float* rstd, void* hip_stream) {
+    return guarded([&]() -> int {
+        Ln p;
+        int rc = validate(prob, &p);
+        if (rc) return rc;
+        const int es = elem_bytes(p.dtype), ps = elem_bytes(p.param);
+        View in[3] = {rows_view("x", x, p.rows, p.xs, p.c, es)}, out[3];
+        int nin = 1, nout = 0;
+        if (gamma) in[nin++] = {"gamma", gamma, p.c * ps, ps};
+        if (beta) in[nin++] = {"beta", beta, p.c * ps, ps};
+        out[nout++] = rows_view("y", y, p.rows, p.ys, p.c, es);
+        if (mean) out[nout++] = {"mean", mean, p.rows * 4, 4};
+        if (rstd) out[nout++] = {"rstd", rstd, p.rows * 4, 4};
+        if ((rc = check_views(in, nin, out, nout))) return rc;
+        if (p.rows == 0) return ok();
+        LnArgs a = ln_args(p);
+        a.x = x;
+        a.gamma = gamma;
+        a.beta = beta;
+        a.y = y;
+        a.mean = mean;
+        a.rstd = rstd;
+        (void)hipGetLastError();
+        launch_layernorm_fwd(p.dtype, p.param, a, reinterpret_cast<hipStream_t>(hip_stream));
+        if ((rc = launched("layernorm_fwd"))) return rc;
+        return ok();
+    });
+}
+
+int cnhwc_layernorm_workspace_size(const cnhwc_layernorm_problem* prob, size_t* bytes) {
+    return guarded([&]() -> int {
+        Ln p;
+        if (int rc = validate(prob, &p)) return rc;
+        if (bytes) *bytes = size_t(ln_part_bytes(p));
+        return ok();
+    });
+}
+
+int cnhwc_layernorm_bwd(const cnhwc_layernorm_problem* prob, const void* dy, const void* x, const void* gamma,
+                        const float* mean, const float* rstd, void* dx, void* dgamma, void* dbeta, void* ws,
+                        size_t ws_bytes, void* hip_stream) {
+    return guarded([&]() -> int {
+        Ln p;
+        int rc = validate(prob, &p);
+        if (rc) return rc;
+        if (!dx && !dgamma && !dbeta) return bad("dx, dgamma and dbeta are all NULL");
+        const int es = elem_bytes(p.dtype), ps = elem_bytes(p.param);
+        View in[5] = {rows_view("dy", dy, p.rows, p.ys, p.c, es), rows_view("x", x, p.rows, p.xs, p.c, es),
+                      {"mean", mean, p.rows * 4, 4}, {"rstd", rstd, p.rows * 4, 4}};
+        View out[4];
+        int nin = 4, nout = 0;
+        if (gamma) in[nin++] = {"gamma", gamma, p.c * ps, ps};
+        if (dx) out[nout++] = rows_view("dx", dx, p.rows, p.xs, p.c, es);
+        if (dgamma) out[nout++] = {"dgamma", dgamma, p.c * ps, ps};
+        if (dbeta) out[nout++] = {"dbeta", dbeta, p.c * ps, ps};
+        const bool cols = dgamma || dbeta;
+        const int64_t need = cols ? ln_part_bytes(p) : 0;
+        if (need > 0) out[nout++] = {"workspace", ws, need, 16};
+        if ((rc = check_views(in, nin, out, nout))) return rc;
+        if (int64_t(ws_bytes) < need)
+            return fail(CNHWC_WORKSPACE_TOO_SMALL,
+                        "workspace needs " + num(need) + " bytes, got " + std::to_string(ws_bytes));
+        hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+        (void)hipGetLastError();
+        const int blocks = layernorm_bwd_blocks(p.dtype, p.rows, p.c);
+        if (p.rows > 0) {
+            LnArgs a = ln_args(p);
+            a.x = x;
+            a.dy = dy;
+            a.gamma = gamma;
+            a.mean = const_cast<float*>(mean);
+            a.rstd = const_cast<float*>(rstd);
+            a.y = dx;
+            a.part = cols ? static_cast<float*>(ws) : nullptr;
+            launch_layernorm_bwd(p.dtype, p.param, a, blocks, st);
+            if ((rc = launched("layernorm_bwd"))) return rc;
+        }
+        if (cols) {
+            launch_layernorm_reduce(p.param, static_cast<const float*>(ws), blocks, p.c, dgamma, dbeta, st);
+            if ((rc = launched("layernorm_reduce"))) return rc;
+        }
+        return ok();
+    });
+}
+
+int cnhwc_gated_workspace_size(const cnhwc_gated_problem* prob, int op, int unaligned, size_t* bytes) {
+    return guarded([&]() -> int {
+        Gated p;
+        if (int rc = validate(prob, &p)) return rc;
+        if (op != CNHWC_OP_FWD && op != CNHWC_OP_DGRAD)
+            return bad("op must be CNHWC_OP_FWD (1) or CNHWC_OP_DGRAD (2, the whole backward pass)");
+        if (bytes) *bytes = size_t(plan_gated(p, op, unaligned != 0, unaligned != 0).bytes);
+        return ok();
+    });
+}
+
+int cnhwc_gated_plan(const cnhwc_gated_problem* prob, int op, char* name, size_t cap) {
+    return guarded([&]() -> int {
+        Gated p;
+        if (int rc = validate(prob, &p)) return rc;
+        if (op != CNHWC_OP_FWD && op != CNHWC_OP_DGRAD)
+            return bad("op must be CNHWC_OP_FWD (1) or CNHWC_OP_DGRAD (2, the whole backward pass)");
+        const GatedPlan g = plan_gated(p, op, false, false);
+        std::string s;
+        if (p.rows == 0) s = "none";
+        else if (g.few_rows) s = std::string("gated_rows_") + dt_name(p.dtype);
+        else {
+            if (g.pack_x || g.pack_w) s = "pack ";
+            s += shape_name("proj", p.dtype, g.proj);
+            if (op != CNHWC_OP_FWD) s += " " + shape_name("dx", p.dtype, g.dx) + " " + shape_name("dw", p.dtype, g.dw);
+        }
+        if (name && cap > 0) {
+            std::strncpy(name, s.c_str(), cap - 1);
+            name[cap - 1] = '\0';
+        }
+        return ok();
+    });
+}
+
+int cnhwc_gated_fwd(const cnhwc_gated_problem* prob, const void* x, const void* wg, const void* wu, void* y, void* ws,
+                    size_t ws_bytes, void* hip_stream) {
+    return guarded([&]() -> int {
+        return run_gated(prob, CNHWC_OP_FWD, nullptr, x, wg, wu, y, nullptr, nullptr, nullptr, ws, ws_bytes,
+                         hip_stream);
+    });
+}
+
+int cnhwc_gated_bwd(const cnhwc_gated_problem* prob, const void* dy, const void* x, const void* wg, const void* wu,
+                    void* dx, void* dwg, void* dwu, void* ws, size_t ws_bytes, void* hip_stream) {
+    return guarded([&]() -> int {
+        return run_gated(prob, CNHWC_OP_DGRAD, dy, x, wg, wu, nullptr, dx, dwg, dwu, ws, ws_bytes, hip_stream);
+    });
+}
+
+int cnhwc_dropout(const cnhwc_dropout_problem* prob, const void* x, const void* residual, void* y,
+                  const uint64_t* device_offset, void* hip_stream) {
+    return guarded([&]() -> int {
+        if (!prob) return bad("problem descriptor is NULL");
+        const cnhwc_dropout_problem& q = *prob;
+        if (q.reserved != 0) return bad("reserved field must be 0");
+        int rc = check_rows(q.rows);
+        if (rc) return rc;
+        if (q.c < 1 || q.c > kMaxI32) return bad("c must be in [1, 2^31) (got " + num(q.c) + ")");
+        if (!(q.p >= 0.0 && q.p <= 1.0)) return bad("p must be in [0, 1]");
+        if (q.dtype != CNHWC_F16 && q.dtype != CNHWC_BF16 && q.dtype != CNHWC_F32)
+            return bad("dtype must be CNHWC_F16, CNHWC_BF16 or CNHWC_F32 (got " + num(q.dtype) + ")");
+        const int es = elem_bytes(q.dtype);
+        DropArgs a;
+        std::memset(&a, 0, sizeof a);
+        if ((rc = check_stride(q.x_stride, q.c, q.rows, es, "x_stride", &a.x_stride))) return rc;
+        if ((rc = check_stride(q.residual_stride, q.c, q.rows, es, "residual_stride", &a.res_stride))) return rc;
+        if ((rc = check_stride(q.y_stride, q.c, q.rows, es, "y_stride", &a.y_stride))) return rc;
+        View in[3] = {rows_view("x", x, q.rows, a.x_stride, q.c, es)};
+        int nin = 1;
+        if (residual) in[nin++] = rows_view("residual", residual, q.rows, a.res_stride, q.c, es);
+        const View yv = rows_view("y", y, q.rows, a.y_stride, q.c, es);
+        if (device_offset) in[nin++] = {"device_offset", device_offset, 8, 8};
+        for (int i = 0; i < nin; ++i)
+            if ((rc = check_view(in[i]))) return rc;
+        if ((rc = check_view(yv))) return rc;
+        for (int i = 0; i < nin; ++i) {
+            // in place: each element is read by the thread that writes it
+            const bool same = (i == 0 && y == x && a.y_stride == a.x_stride) ||
+                              (i == 1 && residual && y == residual && a.y_stride == a.res_stride);
+            if (!same && overlap(yv, in[i])) return bad(std::string("y overlaps ") + in[i].name);
+        }
+        if (q.rows == 0) return ok();
+        a.x = x;
+        a.residual = residual;
+        a.y = y;
+        a.device_offset = device_offset;
+        a.n = q.rows * q.c;
+        a.c = q.c;
+        a.seed = q.seed;
+        a.offset = q.offset;
+        a.threshold = uint64_t(std::nearbyint(q.p * 4294967296.0));
+        a.scale = q.p < 1.0 ? float(1.0 / (1.0 - q.p)) : 0.0f;
+        a.flat = a.x_stride == q.c && a.y_stride == q.c && (!residual || a.res_stride == q.c);
+        (void)hipGetLastError();
+        launch_dropout(q.dtype, a, reinterpret_cast<hipStream_t>(hip_stream));
+        if ((rc = launched("dropout"))) return rc;
+        return ok();
+    });
+}
+
+}  // extern "C"

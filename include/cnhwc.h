@@ -197,6 +197,125 @@ int cnhwc_wgrad(const cnhwc_problem* prob, const void* x, const void* dy, void* 
 int cnhwc_fwd_static_ws(const cnhwc_problem* prob, const void* x, const void* w, void* y,
                         void* hip_stream);
 
+/* ---- channel mixing: layer norm, gated feed-forward, dropout ----------------
+ *
+ * The operators a channels-last block runs around its convolutions.  A tensor
+ * [N][H][W][C] (or [tokens][C]) is `rows` = N*H*W rows of c channels; row r
+ * starts r * stride elements after the base pointer (a stride of 0 means
+ * dense, otherwise stride >= c), so a channel slice of a wider tensor is a
+ * valid operand.  The conventions at the top of this file hold, except that
+ * tensor pointers need only be aligned to their element (4 bytes for the fp32
+ * statistics); workspaces are 16-byte aligned.  `rows` may be 0: outputs with
+ * no rows are left alone and weight gradients become 0.  All sums, statistics
+ * and products accumulate in fp32 and no kernel uses atomics, so a call gives
+ * the same bits every time. */
+
+/* fp32 elements: accepted by the layer norm and the dropout. */
+#define CNHWC_F32 2
+
+/* Layer norm over the channels of each row.
+ *   mean = sum(x) / c, rstd = 1 / sqrt(sum((x - mean)^2) / c + eps)
+ *   y = (x - mean) * rstd * gamma + beta
+ * Valid: 0 <= rows, 1 <= c < 2^31; strides 0 or >= c; eps finite and >= 0; dtype
+ * F16, BF16 or F32; param_dtype (gamma, beta and their gradients) equal to
+ * dtype or F32; reserved == 0. */
+typedef struct cnhwc_layernorm_problem {
+    int64_t rows, c;
+    int64_t x_stride, y_stride;   /* x and dx; y and dy */
+    float eps;
+    int32_t dtype, param_dtype;
+    int32_t reserved;
+} cnhwc_layernorm_problem;
+
+/* Forward.  gamma / beta [c] may be NULL (1 / 0); mean / rstd [rows] fp32 are
+ * written for the backward pass unless NULL. */
+int cnhwc_layernorm_fwd(const cnhwc_layernorm_problem* prob, const void* x, const void* gamma,
+                        const void* beta, void* y, float* mean, float* rstd, void* hip_stream);
+
+/* Workspace bytes of cnhwc_layernorm_bwd when dgamma or dbeta is asked for:
+ * the fp32 partial column sums of the blocks. */
+int cnhwc_layernorm_workspace_size(const cnhwc_layernorm_problem* prob, size_t* bytes);
+
+/* Backward.  With xhat = (x - mean) * rstd and g = dy * gamma:
+ *   dx     = rstd * (g - sum(g) / c - xhat * sum(g * xhat) / c)
+ *   dgamma = sum over rows of dy * xhat,   dbeta = sum over rows of dy
+ * mean and rstd are the forward pass's; gamma may be NULL (1).  Each of dx,
+ * dgamma, dbeta may be NULL and is then not computed (not all three).  ws may
+ * be NULL when neither dgamma nor dbeta is asked for. */
+int cnhwc_layernorm_bwd(const cnhwc_layernorm_problem* prob, const void* dy, const void* x,
+                        const void* gamma, const float* mean, const float* rstd, void* dx,
+                        void* dgamma, void* dbeta, void* ws, size_t ws_bytes, void* hip_stream);
+
+/* Gated feed-forward: both widening projections, the activation and the
+ * product in one pass,
+ *   g = x wg^T, u = x wu^T, y = act(g) * u
+ * x [rows][c], wg and wu [f][c] (dense: the filters of two pointwise
+ * convolutions), y [rows][f].  No bias, as in the convolutions here; the
+ * narrowing projection that follows is a pointwise cnhwc_fwd.  g and u stay in
+ * fp32 and are never stored; y is rounded once. */
+#define CNHWC_ACT_SILU 0      /* g / (1 + exp(-g)) */
+#define CNHWC_ACT_GELU 1      /* g * (1 + erf(g / sqrt 2)) / 2 */
+#define CNHWC_ACT_RELU 2      /* max(g, 0), slope 0 at 0 */
+#define CNHWC_ACT_SIGMOID 3   /* 1 / (1 + exp(-g)) */
+
+/* Valid: 0 <= rows < 2^31; 1 <= c, f <= 2^20; strides 0 or >= c (x, dx) and
+ * >= f (y, dy), at most 2^21; act one of the above; dtype F16 or BF16;
+ * reserved == 0. */
+typedef struct cnhwc_gated_problem {
+    int64_t rows, c, f;
+    int64_t x_stride, y_stride;   /* x and dx; y and dy */
+    int32_t act, dtype;
+    int32_t reserved;
+} cnhwc_gated_problem;
+
+/* Workspace bytes of pass `op` (CNHWC_OP_FWD, or CNHWC_OP_DGRAD for the whole
+ * backward pass): operands copied to rows of a multiple of 8 elements where c
+ * or a stride is not one, fp32 partial sums of split reductions and, for the
+ * backward pass, dg and du.  Base pointers off a 16-byte boundary need the
+ * copies as well: `unaligned` != 0 sizes for any pointers. */
+int cnhwc_gated_workspace_size(const cnhwc_gated_problem* prob, int op, int unaligned, size_t* bytes);
+
+/* Names the kernels that pass `op` runs on 16-byte-aligned operands (NUL-terminated, truncated to cap). */
+int cnhwc_gated_plan(const cnhwc_gated_problem* prob, int op, char* name, size_t cap);
+
+int cnhwc_gated_fwd(const cnhwc_gated_problem* prob, const void* x, const void* wg, const void* wu,
+                    void* y, void* ws, size_t ws_bytes, void* hip_stream);
+
+/* Backward.  g and u are computed again from x; then
+ *   dg = dy * u * act'(g), du = dy * act(g)
+ *   dx = dg wg + du wu, dwg = dg^T x, dwu = du^T x
+ * dg and du are rounded to dtype between the two steps: they are operands of
+ * matrix instructions.  dx may be NULL; dwg and dwu may both be NULL. */
+int cnhwc_gated_bwd(const cnhwc_gated_problem* prob, const void* dy, const void* x, const void* wg,
+                    const void* wu, void* dx, void* dwg, void* dwu, void* ws, size_t ws_bytes,
+                    void* hip_stream);
+
+/* Dropout with a mask that is drawn again wherever it is needed:
+ *   y = residual + (keep ? x / (1 - p) : 0)
+ * Element i = row * c + column keeps its value when word i % 4 of
+ * Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy
+ * as 1, 2, 3") at counter (i / 4, offset) and key `seed` is >= p * 2^32
+ * rounded to an integer; the mask does not depend on the strides.  A dropped
+ * element is 0 whatever x holds there (NaN and infinities too), and p = 1 drops
+ * every element.  The backward pass is the same call on dy without a
+ * residual.  Valid: 0 <= rows; 1 <= c < 2^31, rows * c < 2^62; strides 0 or >= c;
+ * 0 <= p <= 1; dtype F16, BF16 or F32; reserved == 0.  y may be x or residual
+ * itself (same pointer and stride); other overlap is refused. */
+typedef struct cnhwc_dropout_problem {
+    int64_t rows, c;
+    int64_t x_stride, residual_stride, y_stride;
+    double p;
+    uint64_t seed, offset;
+    int32_t dtype;
+    int32_t reserved;
+} cnhwc_dropout_problem;
+
+/* residual may be NULL (0).  device_offset, if not NULL, points to one 64-bit
+ * integer on the device that is added to `offset` when the kernel runs, so
+ * that a captured graph draws a new mask on each replay. */
+int cnhwc_dropout(const cnhwc_dropout_problem* prob, const void* x, const void* residual, void* y,
+                  const uint64_t* device_offset, void* hip_stream);
+
 /* Reason for the last non-zero status on this thread ("" after success).  The
  * checks run in a fixed order and the first failing one is reported, as the
  * pages' C++ engine keeps its validators in the same order and with the same
@@ -230,8 +349,9 @@ const char* cnhwc_last_error(void);
  * chunk; depthwise rotated-filter: 1 runs one tap group, 2 two groups, both
  * with 8-column filter slices even for filters narrower than 8 columns;
  * depthwise LDS-tiled (dgrad and forward): 1 keeps 7x7 filters on the
- * one-tile-per-block kernel instead of the persistent one; other kernels
- * ignore it);
+ * one-tile-per-block kernel instead of the persistent one; gated feed-forward:
+ * 128 or 256 forces the tile of its products, split_c their reduction splits;
+ * other kernels ignore it);
  * chunk_limit_bytes: the per-view byte limit of the chunk planner.  Pass NULL
  * to clear. */
 typedef struct cnhwc_override {

@@ -1,7 +1,7 @@
 // The matrix products of the gated feed-forward block on MFMA.
 //
-// One kernel serves the three products of gated.h.  A block computes a tile
-// of 2*HM rows by 2*HN columns (HM = HN = 128 with 8 waves, 64 with 4); each
+// One kernel serves the three products of gated.h.  A block computes tiles of
+// 2*HM rows by 2*HN columns (HM = HN = 128 with 8 waves, 64 with 4); each
 // operand's 64-deep slice of the tile is two half tiles in LDS, and a wave
 // owns the same quarter of every half, so its result is four quadrants
 // (row half, column half).  In PROJ the column halves are the same hidden
@@ -9,34 +9,36 @@
 // and the activation and product (or, backward, dg and du) follow without
 // another pass over memory.
 //
-// A step of the reduction runs in four phases, one quadrant each:
-//     phase   reads into registers   multiplies
-//       0     row half 0             (0, 0)
-//       1     column half 1          (0, 1)
-//       2     row half 1             (1, 1)
-//       3     column half 0 of the   (1, 0)
-//             next step
-// so every half tile is read once and its LDS is free one phase later, where
-// the asynchronous loads of the step after next refill it: with two stages a
-// load has seven phases to land, and every phase's wait allows the same
-// twelve younger loads in flight.  The 8-wave block runs its two halves of
-// waves (one wave of each on every SIMD) half a phase apart, with a barrier on
-// each side of the multiplications: while one wave of a SIMD multiplies, the
-// other reads and issues loads.  The 4-wave block needs one barrier a phase
-// and overlaps with the second block of its CU instead.
+// A step of the reduction runs in two phases, one row half each:
+//     phase   reads into registers                         multiplies row half
+//       0     row half 0, column half 1                            0
+//       1     row half 1, column half 0 of the next step           1
+// so the two phases read the same amount, every half tile is read once, and
+// its LDS is free one phase later, where the asynchronous loads of the step
+// after next (row half 1: of the next) refill it.  With two stages a load has
+// two phases to land; every phase's wait allows the eight younger loads.  The
+// 8-wave block runs its two halves of waves (one wave of each on every SIMD)
+// half a phase apart, with a barrier on each side of the multiplications:
+// while one wave of a SIMD multiplies, the other reads and issues loads.  The
+// 4-wave block needs one barrier a phase and overlaps with the second block of
+// its CU instead.
+//
+// Blocks are persistent: the loads run on into a block's next tile while the
+// current one is rounded and stored, so a tile's first operands are there when
+// its turn comes, and its stores drain under the next tile's products.
 //
 // A half tile whose rows are contiguous in the reduction (x, wg, wu in PROJ;
 // dg | du in DX) lies in LDS as rows of 64 elements, read with 16-byte reads;
 // one whose rows are the reduction (wg, wu in DX; both operands of DW) as 64
 // rows of HM or HN elements, read with the transposing read.  16- or 32-byte
 // units are exchanged by an exclusive-or with row bits so that the lanes of a
-// read spread over all banks; the exchange is done by the load's source
-// address.
+// read spread over all banks (no conflicts counted); the exchange is done by
+// the load's source address.
 //
-// Addresses: each half tile's source is a buffer view rebuilt every step from
-// a 64-bit base, so neither tensor size nor row count is limited by 32-bit
-// offsets; rows past an operand's end read as zero by the view's length,
-// columns past the reduction's end by an out-of-range offset.
+// Addresses: a tile's operands are buffer views on 64-bit bases, so neither
+// tensor size nor row count is limited by 32-bit offsets; rows past an
+// operand's end read as zero by the view's length, columns past the
+// reduction's end by an out-of-range offset.
 #include "gated.h"
 
 namespace cnhwc {
@@ -44,302 +46,469 @@ namespace {
 
 constexpr int kBK = 64;   // reduction depth of a step
 
-// Reads of one quadrant operand: NT 16-row tiles by two 32-deep products, all
-// landed when the block ends (one asm block with its wait, so no register of
-// it is live while a read is in flight).  p0 / p1: this lane's address for the
-// first and second product; OFF: byte offset; TS: bytes from tile to tile.
-template <int NT, int OFF, int TS>
-__device__ __attribute__((always_inline)) inline void read_rows(i32x4 (&r)[NT][2], uint32_t p0, uint32_t p1) {
-    if constexpr (NT == 4)
-        asm volatile(
-            "ds_read_b128 %0, %8 offset:%10\n\t"
-            "ds_read_b128 %1, %9 offset:%10\n\t"
-            "ds_read_b128 %2, %8 offset:%11\n\t"
-            "ds_read_b128 %3, %9 offset:%11\n\t"
-            "ds_read_b128 %4, %8 offset:%12\n\t"
-            "ds_read_b128 %5, %9 offset:%12\n\t"
-            "ds_read_b128 %6, %8 offset:%13\n\t"
-            "ds_read_b128 %7, %9 offset:%13\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[2][0]), "=&v"(r[2][1]),
-              "=&v"(r[3][0]), "=&v"(r[3][1])
-            : "v"(p0), "v"(p1), "i"(OFF), "i"(OFF + TS), "i"(OFF + 2 * TS), "i"(OFF + 3 * TS)
-            : "memory");
-    else
-        asm volatile(
-            "ds_read_b128 %0, %4 offset:%6\n\t"
-            "ds_read_b128 %1, %5 offset:%6\n\t"
-            "ds_read_b128 %2, %4 offset:%7\n\t"
-            "ds_read_b128 %3, %5 offset:%7\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1])
-            : "v"(p0), "v"(p1), "i"(OFF), "i"(OFF + TS)
-            : "memory");
-}
+// ---- LDS reads and loads -----------------------------------------------------------
+//
+// What one phase moves: a row half into a (Q 16-row tiles by two 32-deep
+// products, from offset OA) and a column half into b (two tiles, from offset
+// OB), by the layouts of the two operands; then, while those reads run, the
+// loads of two half tiles are issued.  Each function is one asm block that ends
+// with its wait, so no register of it is live while a read is in flight; the
+// loads write LDS only.  (Issued before the reads, the loads held them up: a
+// CU takes one KiB in 16 cycles, four waves' loads of a phase in 260.)
+//
+// Rows contiguous in the reduction: p[0] / p[1] address the first and second
+// product, tiles follow 2048 bytes apart in a and 512 in b (whose tiles
+// interleave by 4 rows).  Rows that are the reduction (transposing reads, 4
+// consecutive k a read): p[tile], HB bytes to k + 4, KB to the second product.
 
-// The same with the transposing read, two tiles at a time: a lane gets 4
-// consecutive k of its column per read, KB bytes apart for the second product
-// and HB bytes for k + 4.
-template <int OFF, int KB, int HB>
-__device__ __attribute__((always_inline)) inline void read_cols2(i32x4 (&r0)[2], i32x4 (&r1)[2], uint32_t p0,
-                                                                 uint32_t p1) {
-    i32x2 a, b, c, d, e, f, g, h;
+// This wave's two loads of a half tile: view, per-lane offsets, offset of the
+// step, and the first one's LDS address (the second goes one KiB on).
+struct Load {
+    i32x4 r;
+    uint32_t v[2];
+    uint32_t s;
+    uint32_t to;
+};
+
+#define CNHWC_RD(d, a, o) "ds_read_b128 %" #d ", %" #a " offset:%" #o "\n\t"
+#define CNHWC_TR(d, a, o) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:%" #o "\n\t"
+#define CNHWC_LD(r, v0, v1, so, to)                                                    \
+    "s_mov_b32 m0, %" #to "\n\ts_nop 0\n\tbuffer_load_dwordx4 %" #v0 ", %" #r ", %" #so \
+    " offen lds\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tbuffer_load_dwordx4 %" #v1  \
+    ", %" #r ", %" #so " offen lds\n\t"
+
+__device__ __attribute__((always_inline)) inline i32x4 join(i32x2 a, i32x2 b) { return i32x4{a[0], a[1], b[0], b[1]}; }
+
+// b alone
+template <int OB>
+__device__ __attribute__((always_inline)) inline void read_rows(i32x4 (&b)[2][2], const uint32_t (&pb)[2]) {
+    asm volatile(CNHWC_RD(0, 4, 6) CNHWC_RD(1, 5, 6) CNHWC_RD(2, 4, 7) CNHWC_RD(3, 5, 7) "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(b[0][0]), "=&v"(b[0][1]), "=&v"(b[1][0]), "=&v"(b[1][1])
+                 : "v"(pb[0]), "v"(pb[1]), "i"(OB), "i"(OB + 512)
+                 : "memory");
+}
+template <int OB, int HB, int KB>
+__device__ __attribute__((always_inline)) inline void read_cols(i32x4 (&b)[2][2], const uint32_t (&pb)[2]) {
+    i32x2 t[8];
+    asm volatile(CNHWC_TR(0, 8, 10) CNHWC_TR(1, 8, 11) CNHWC_TR(2, 8, 12) CNHWC_TR(3, 8, 13) CNHWC_TR(4, 9, 10)
+                     CNHWC_TR(5, 9, 11) CNHWC_TR(6, 9, 12) CNHWC_TR(7, 9, 13) "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3]), "=&v"(t[4]), "=&v"(t[5]), "=&v"(t[6]),
+                   "=&v"(t[7])
+                 : "v"(pb[0]), "v"(pb[1]), "i"(OB), "i"(OB + HB), "i"(OB + KB), "i"(OB + KB + HB)
+                 : "memory");
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) b[j][k] = join(t[4 * j + 2 * k], t[4 * j + 2 * k + 1]);
+}
+// a and b, and the loads
+template <int OA, int OB>
+__device__ __attribute__((always_inline)) inline void read_rows_rows(i32x4 (&a)[4][2], i32x4 (&b)[2][2], const uint32_t (&pa)[2],
+                                                                 const uint32_t (&pb)[2], const Load& d0, const Load& d1) {
     asm volatile(
-        "ds_read_b64_tr_b16 %0, %8 offset:%10\n\t"
-        "ds_read_b64_tr_b16 %1, %8 offset:%11\n\t"
-        "ds_read_b64_tr_b16 %2, %8 offset:%12\n\t"
-        "ds_read_b64_tr_b16 %3, %8 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %4, %9 offset:%10\n\t"
-        "ds_read_b64_tr_b16 %5, %9 offset:%11\n\t"
-        "ds_read_b64_tr_b16 %6, %9 offset:%12\n\t"
-        "ds_read_b64_tr_b16 %7, %9 offset:%13\n\t"
+        CNHWC_RD(0, 14, 30) CNHWC_RD(1, 15, 30) CNHWC_RD(2, 14, 31) CNHWC_RD(3, 15, 31) CNHWC_RD(4, 12, 26)
+        CNHWC_RD(5, 13, 26) CNHWC_RD(6, 12, 27) CNHWC_RD(7, 13, 27) CNHWC_RD(8, 12, 28) CNHWC_RD(9, 13, 28)
+        CNHWC_RD(10, 12, 29) CNHWC_RD(11, 13, 29) CNHWC_LD(16, 17, 18, 19, 20) CNHWC_LD(21, 22, 23, 24, 25)
         "s_waitcnt lgkmcnt(0)"
-        : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h)
-        : "v"(p0), "v"(p1), "i"(OFF), "i"(OFF + HB), "i"(OFF + KB), "i"(OFF + KB + HB)
-        : "memory");
-    r0[0] = i32x4{a[0], a[1], b[0], b[1]};
-    r0[1] = i32x4{c[0], c[1], d[0], d[1]};
-    r1[0] = i32x4{e[0], e[1], f[0], f[1]};
-    r1[1] = i32x4{g[0], g[1], h[0], h[1]};
+        : "=&v"(b[0][0]), "=&v"(b[0][1]), "=&v"(b[1][0]), "=&v"(b[1][1]), "=&v"(a[0][0]), "=&v"(a[0][1]),
+          "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(a[2][0]), "=&v"(a[2][1]), "=&v"(a[3][0]), "=&v"(a[3][1])
+        : "v"(pa[0]), "v"(pa[1]), "v"(pb[0]), "v"(pb[1]), "s"(d0.r), "v"(d0.v[0]), "v"(d0.v[1]), "s"(d0.s),
+          "s"(d0.to), "s"(d1.r), "v"(d1.v[0]), "v"(d1.v[1]), "s"(d1.s), "s"(d1.to), "i"(OA), "i"(OA + 2048),
+          "i"(OA + 4096), "i"(OA + 6144), "i"(OB), "i"(OB + 512)
+        : "memory", "m0", "scc");
 }
+template <int OA, int OB, int HB, int KB>
+__device__ __attribute__((always_inline)) inline void read_rows_cols(i32x4 (&a)[4][2], i32x4 (&b)[2][2], const uint32_t (&pa)[2],
+                                                                 const uint32_t (&pb)[2], const Load& d0, const Load& d1) {
+    i32x2 t[8];
+    asm volatile(
+        CNHWC_TR(0, 18, 34) CNHWC_TR(1, 18, 35) CNHWC_TR(2, 18, 36) CNHWC_TR(3, 18, 37) CNHWC_TR(4, 19, 34)
+        CNHWC_TR(5, 19, 35) CNHWC_TR(6, 19, 36) CNHWC_TR(7, 19, 37) CNHWC_RD(8, 16, 30) CNHWC_RD(9, 17, 30)
+        CNHWC_RD(10, 16, 31) CNHWC_RD(11, 17, 31) CNHWC_RD(12, 16, 32) CNHWC_RD(13, 17, 32)
+        CNHWC_RD(14, 16, 33) CNHWC_RD(15, 17, 33) CNHWC_LD(20, 21, 22, 23, 24) CNHWC_LD(25, 26, 27, 28, 29)
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3]), "=&v"(t[4]), "=&v"(t[5]), "=&v"(t[6]), "=&v"(t[7]),
+          "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(a[2][0]), "=&v"(a[2][1]),
+          "=&v"(a[3][0]), "=&v"(a[3][1])
+        : "v"(pa[0]), "v"(pa[1]), "v"(pb[0]), "v"(pb[1]), "s"(d0.r), "v"(d0.v[0]), "v"(d0.v[1]), "s"(d0.s),
+          "s"(d0.to), "s"(d1.r), "v"(d1.v[0]), "v"(d1.v[1]), "s"(d1.s), "s"(d1.to), "i"(OA), "i"(OA + 2048),
+          "i"(OA + 4096), "i"(OA + 6144), "i"(OB), "i"(OB + HB), "i"(OB + KB), "i"(OB + KB + HB)
+        : "memory", "m0", "scc");
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) b[j][k] = join(t[4 * j + 2 * k], t[4 * j + 2 * k + 1]);
+}
+template <int OA, int OB, int HB, int KB>
+__device__ __attribute__((always_inline)) inline void read_cols_cols(i32x4 (&a)[4][2], i32x4 (&b)[2][2], const uint32_t (&pa)[4],
+                                                                 const uint32_t (&pb)[2], const Load& d0, const Load& d1) {
+    i32x2 t[24];
+    asm volatile(
+        CNHWC_TR(0, 28, 44) CNHWC_TR(1, 28, 45) CNHWC_TR(2, 28, 46) CNHWC_TR(3, 28, 47) CNHWC_TR(4, 29, 44)
+        CNHWC_TR(5, 29, 45) CNHWC_TR(6, 29, 46) CNHWC_TR(7, 29, 47) CNHWC_TR(8, 24, 40) CNHWC_TR(9, 24, 41)
+        CNHWC_TR(10, 24, 42) CNHWC_TR(11, 24, 43) CNHWC_TR(12, 25, 40) CNHWC_TR(13, 25, 41)
+        CNHWC_TR(14, 25, 42) CNHWC_TR(15, 25, 43) CNHWC_TR(16, 26, 40) CNHWC_TR(17, 26, 41)
+        CNHWC_TR(18, 26, 42) CNHWC_TR(19, 26, 43) CNHWC_TR(20, 27, 40) CNHWC_TR(21, 27, 41)
+        CNHWC_TR(22, 27, 42) CNHWC_TR(23, 27, 43) CNHWC_LD(30, 31, 32, 33, 34) CNHWC_LD(35, 36, 37, 38, 39)
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3]), "=&v"(t[4]), "=&v"(t[5]), "=&v"(t[6]), "=&v"(t[7]),
+          "=&v"(t[8]), "=&v"(t[9]), "=&v"(t[10]), "=&v"(t[11]), "=&v"(t[12]), "=&v"(t[13]), "=&v"(t[14]),
+          "=&v"(t[15]), "=&v"(t[16]), "=&v"(t[17]), "=&v"(t[18]), "=&v"(t[19]), "=&v"(t[20]), "=&v"(t[21]),
+          "=&v"(t[22]), "=&v"(t[23])
+        : "v"(pa[0]), "v"(pa[1]), "v"(pa[2]), "v"(pa[3]), "v"(pb[0]), "v"(pb[1]), "s"(d0.r), "v"(d0.v[0]),
+          "v"(d0.v[1]), "s"(d0.s), "s"(d0.to), "s"(d1.r), "v"(d1.v[0]), "v"(d1.v[1]), "s"(d1.s), "s"(d1.to),
+          "i"(OA), "i"(OA + HB), "i"(OA + KB), "i"(OA + KB + HB), "i"(OB), "i"(OB + HB), "i"(OB + KB), "i"(OB + KB
+          + HB)
+        : "memory", "m0", "scc");
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) b[j][k] = join(t[4 * j + 2 * k], t[4 * j + 2 * k + 1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) a[i][k] = join(t[8 + 4 * i + 2 * k], t[9 + 4 * i + 2 * k]);
+}
+template <int OA, int OB>
+__device__ __attribute__((always_inline)) inline void read_rows_rows(i32x4 (&a)[2][2], i32x4 (&b)[2][2], const uint32_t (&pa)[2],
+                                                                 const uint32_t (&pb)[2], const Load& d0, const Load& d1) {
+    asm volatile(
+        CNHWC_RD(0, 10, 24) CNHWC_RD(1, 11, 24) CNHWC_RD(2, 10, 25) CNHWC_RD(3, 11, 25) CNHWC_RD(4, 8, 22)
+        CNHWC_RD(5, 9, 22) CNHWC_RD(6, 8, 23) CNHWC_RD(7, 9, 23) CNHWC_LD(12, 13, 14, 15, 16)
+        CNHWC_LD(17, 18, 19, 20, 21) "s_waitcnt lgkmcnt(0)"
+        : "=&v"(b[0][0]), "=&v"(b[0][1]), "=&v"(b[1][0]), "=&v"(b[1][1]), "=&v"(a[0][0]), "=&v"(a[0][1]),
+          "=&v"(a[1][0]), "=&v"(a[1][1])
+        : "v"(pa[0]), "v"(pa[1]), "v"(pb[0]), "v"(pb[1]), "s"(d0.r), "v"(d0.v[0]), "v"(d0.v[1]), "s"(d0.s),
+          "s"(d0.to), "s"(d1.r), "v"(d1.v[0]), "v"(d1.v[1]), "s"(d1.s), "s"(d1.to), "i"(OA), "i"(OA + 2048),
+          "i"(OB), "i"(OB + 512)
+        : "memory", "m0", "scc");
+}
+template <int OA, int OB, int HB, int KB>
+__device__ __attribute__((always_inline)) inline void read_rows_cols(i32x4 (&a)[2][2], i32x4 (&b)[2][2], const uint32_t (&pa)[2],
+                                                                 const uint32_t (&pb)[2], const Load& d0, const Load& d1) {
+    i32x2 t[8];
+    asm volatile(
+        CNHWC_TR(0, 14, 28) CNHWC_TR(1, 14, 29) CNHWC_TR(2, 14, 30) CNHWC_TR(3, 14, 31) CNHWC_TR(4, 15, 28)
+        CNHWC_TR(5, 15, 29) CNHWC_TR(6, 15, 30) CNHWC_TR(7, 15, 31) CNHWC_RD(8, 12, 26) CNHWC_RD(9, 13, 26)
+        CNHWC_RD(10, 12, 27) CNHWC_RD(11, 13, 27) CNHWC_LD(16, 17, 18, 19, 20) CNHWC_LD(21, 22, 23, 24, 25)
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3]), "=&v"(t[4]), "=&v"(t[5]), "=&v"(t[6]), "=&v"(t[7]),
+          "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1])
+        : "v"(pa[0]), "v"(pa[1]), "v"(pb[0]), "v"(pb[1]), "s"(d0.r), "v"(d0.v[0]), "v"(d0.v[1]), "s"(d0.s),
+          "s"(d0.to), "s"(d1.r), "v"(d1.v[0]), "v"(d1.v[1]), "s"(d1.s), "s"(d1.to), "i"(OA), "i"(OA + 2048),
+          "i"(OB), "i"(OB + HB), "i"(OB + KB), "i"(OB + KB + HB)
+        : "memory", "m0", "scc");
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) b[j][k] = join(t[4 * j + 2 * k], t[4 * j + 2 * k + 1]);
+}
+template <int OA, int OB, int HB, int KB>
+__device__ __attribute__((always_inline)) inline void read_cols_cols(i32x4 (&a)[2][2], i32x4 (&b)[2][2], const uint32_t (&pa)[2],
+                                                                 const uint32_t (&pb)[2], const Load& d0, const Load& d1) {
+    i32x2 t[16];
+    asm volatile(
+        CNHWC_TR(0, 18, 34) CNHWC_TR(1, 18, 35) CNHWC_TR(2, 18, 36) CNHWC_TR(3, 18, 37) CNHWC_TR(4, 19, 34)
+        CNHWC_TR(5, 19, 35) CNHWC_TR(6, 19, 36) CNHWC_TR(7, 19, 37) CNHWC_TR(8, 16, 30) CNHWC_TR(9, 16, 31)
+        CNHWC_TR(10, 16, 32) CNHWC_TR(11, 16, 33) CNHWC_TR(12, 17, 30) CNHWC_TR(13, 17, 31)
+        CNHWC_TR(14, 17, 32) CNHWC_TR(15, 17, 33) CNHWC_LD(20, 21, 22, 23, 24) CNHWC_LD(25, 26, 27, 28, 29)
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(t[0]), "=&v"(t[1]), "=&v"(t[2]), "=&v"(t[3]), "=&v"(t[4]), "=&v"(t[5]), "=&v"(t[6]), "=&v"(t[7]),
+          "=&v"(t[8]), "=&v"(t[9]), "=&v"(t[10]), "=&v"(t[11]), "=&v"(t[12]), "=&v"(t[13]), "=&v"(t[14]),
+          "=&v"(t[15])
+        : "v"(pa[0]), "v"(pa[1]), "v"(pb[0]), "v"(pb[1]), "s"(d0.r), "v"(d0.v[0]), "v"(d0.v[1]), "s"(d0.s),
+          "s"(d0.to), "s"(d1.r), "v"(d1.v[0]), "v"(d1.v[1]), "s"(d1.s), "s"(d1.to), "i"(OA), "i"(OA + HB), "i"(OA
+          + KB), "i"(OA + KB + HB), "i"(OB), "i"(OB + HB), "i"(OB + KB), "i"(OB + KB + HB)
+        : "memory", "m0", "scc");
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) b[j][k] = join(t[4 * j + 2 * k], t[4 * j + 2 * k + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) a[i][k] = join(t[8 + 4 * i + 2 * k], t[9 + 4 * i + 2 * k]);
+}
+#undef CNHWC_RD
+#undef CNHWC_TR
+#undef CNHWC_LD
 
-// One operand of the tile: where its half tiles come from.  ROWS: contiguous
-// in the reduction.  PERM: its rows are read in the order that gives a lane 8
-// consecutive ones over two tiles (the result's columns).
+// ---- one operand of the tile --------------------------------------------------------
+
+// Where this lane's loads of its wave's two 1 KiB regions of a half tile come
+// from.  ROWS: the operand's rows are contiguous in the reduction.  PERM: its
+// rows are read in the order that gives a lane 8 consecutive ones over two
+// 16-row tiles (the result's columns).  HALF: rows (ROWS) or columns of a half.
 template <bool ROWS, bool PERM, int HALF>
 struct Operand {
-    const char* base[2];   // half 0 / 1 at the current step
-    const char* end[2];
-    int64_t step;          // bytes from step to step
-    uint32_t voff[2];      // this lane's offset in its wave's two 1 KiB regions
-    int kc;                // ROWS: this lane's k within the step
+    uint32_t voff[2];   // byte offset in the first half; the second is `half` on
+    uint32_t half;
+    int lane_k[2];      // ROWS: its k within a step
 
-    __device__ __attribute__((always_inline)) void lanes(int wave, int lane, int64_t ld) {
+    __device__ __attribute__((always_inline)) Operand(int wave, int lane, int64_t ld) {
+        half = uint32_t(ROWS ? HALF * ld * 2 : HALF * 2);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int region = wave * 2 + q;
             if constexpr (ROWS) {
                 const int row = region * 8 + (lane >> 3);
-                const int swz = PERM ? ((row & 3) | ((row >> 1) & 4)) : (row & 7);
-                voff[q] = uint32_t(row * ld * 2 + (((lane & 7) ^ swz) << 4));
+                const int unit = (lane & 7) ^ (PERM ? ((row & 3) | ((row >> 1) & 4)) : (row & 7));
+                voff[q] = uint32_t(row * ld * 2 + unit * 16);
+                lane_k[q] = unit * 8;
             } else {
-                constexpr int CH = HALF / 8;   // 16-byte units of a row
-                const int k = region * (64 / CH) + lane / CH, pos = lane % CH;
-                voff[q] = uint32_t(k * ld * 2 + ((((pos >> 1) ^ kswz(k)) << 5) | ((pos & 1) << 4)));
+                constexpr int U = HALF / 8;   // 16-byte units of a row
+                const int k = region * (64 / U) + lane / U, pos = lane % U;
+                voff[q] = uint32_t(k * ld * 2 + ((((pos >> 1) ^ swz(k)) << 5) | ((pos & 1) << 4)));
+                lane_k[q] = 0;
             }
         }
-        kc = 0;
     }
-    // exchange of 32-byte units in a row of HALF elements
-    __device__ static int kswz(int k) {
+    // which 32-byte unit of a row of HALF elements moves where
+    __device__ static int swz(int k) {
         if constexpr (HALF == 128) return (k & 3) | ((k >> 1) & 4);
         else return ((k >> 1) & 1) | ((k >> 2) & 2);
     }
-    // this lane's k within a step for region q
-    __device__ __attribute__((always_inline)) static int lane_k(int wave, int lane, int q) {
-        const int row = (wave * 2 + q) * 8 + (lane >> 3);
-        const int swz = PERM ? ((row & 3) | ((row >> 1) & 4)) : (row & 7);
-        return ((lane & 7) ^ swz) * 8;
-    }
 };
+
+// The kernel's arguments read again from where they were passed: what only a
+// tile's start and end need is not held in scalar registers over its steps
+// (nor anything computed from it before the loop).
+typedef const __attribute__((address_space(4))) GatedArgs ArgsMem;
+__device__ __attribute__((always_inline)) inline ArgsMem& args_again() {
+    auto p = (ArgsMem*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *p;
+}
+
+struct Tile {
+    int64_t m0, n0;
+    int split, s_lo, steps;
+};
+
+// The v-th tile of the launch: consecutive tiles on one XCD (blocks go round
+// the 8 XCDs in turn), in groups of 8 tile rows so that the tiles at work on
+// an XCD share operands in its L2.
+template <int TILE, int NT>
+__device__ __attribute__((always_inline)) inline Tile tile_of(int v) {
+    ArgsMem& a = args_again();
+    const int tiles = a.tiles_m * a.tiles_n, total = tiles * a.splits;
+    const int x = v & 7, base = total >> 3, rem = total & 7;
+    const int id = x * base + (x < rem ? x : rem) + (v >> 3);
+    Tile t;
+    t.split = id / tiles;
+    const int r0 = id - t.split * tiles;
+    const int per = 8 * a.tiles_n, grp = r0 / per, r = r0 - grp * per;
+    const int rows = a.tiles_m - grp * 8 < 8 ? a.tiles_m - grp * 8 : 8;
+    const int tn = r / rows, tm = grp * 8 + (r - tn * rows);
+    t.m0 = int64_t(tm) * TILE;
+    t.n0 = int64_t(tn) * NT;
+    const int all = a.segs * a.steps_seg;
+    // (at most 2^25 steps and 64 splits)
+    t.s_lo = int(uint32_t(all) * uint32_t(t.split) / uint32_t(a.splits));
+    t.steps = int(uint32_t(all) * uint32_t(t.split + 1) / uint32_t(a.splits)) - t.s_lo;
+    return t;
+}
+
+__device__ __attribute__((always_inline)) inline __amdgpu_buffer_rsrc_t view(const char* p, int64_t n) {
+    return make_rsrc(p, n > 0 ? (n < 0x7fffffff ? uint32_t(n) : 0x7fffffffu) : 0u);
+}
+
+// Results stay in the caches: the next product or operator reads them.
+__device__ __attribute__((always_inline)) inline void store16_at(i32x4 v, __amdgpu_buffer_rsrc_t r, uint32_t off) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+}
 
 // END: what follows the products (a GatedEnd); ACT only where PROD is kProj.
 template <typename T, int PROD, int TILE, int END, int ACT>
 __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_kernel(const GatedArgs a) {
     constexpr bool AROWS = PROD != kDw, BROWS = PROD == kProj;
-    constexpr int WN = TILE / 64, WAVES = 2 * WN;     // waves: 2 over rows, WN over columns
+    constexpr int WN = TILE / 64;                     // waves: 2 over rows, WN over columns
     constexpr int HALF = TILE / 2;                    // rows / columns of a half tile
+    constexpr int NT = PROD == kProj ? HALF : TILE;   // result columns of a tile
     constexpr int QM = HALF / 32;                     // 16-row tiles of a quadrant; 2 tiles of columns
     constexpr bool PP = TILE == kGatedBig;            // two wave groups half a phase apart
     constexpr int HBYTES = HALF * 128;                // a half tile in LDS
     constexpr int BBASE = 4 * HBYTES;                 // A: [half][stage], then B
+    // stores of a tile's results per wave, all of them issued whatever the
+    // tile's edges (the offsets past them are out of range): the waits of the
+    // next tile's first step count over them
+    constexpr int STORES = END == kEndPart ? 0 : PROD == kProj ? 2 * QM * (END == kEndBwd ? 2 : 1) : 4 * QM;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[8 * HBYTES];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
+    const int total = a.tiles_m * a.tiles_n * a.splits;
 
-    // ---- block -> tile: consecutive tiles on one XCD (blocks go round the 8
-    // XCDs in turn), in groups of 8 tile rows so that the tiles at work on an
-    // XCD share operands in its L2
-    const int tiles = a.tiles_m * a.tiles_n;
-    const int total = tiles * a.splits;
-    int id = blockIdx.x;
-    {
-        const int x = id & 7, q = id >> 3, base = total >> 3, rem = total & 7;
-        id = x * base + (x < rem ? x : rem) + q;
-    }
-    const int split = id / tiles;
-    int tm, tn;
-    {
-        const int t = id - split * tiles;
-        const int per = 8 * a.tiles_n, grp = t / per, r = t - grp * per;
-        const int rows = a.tiles_m - grp * 8 < 8 ? a.tiles_m - grp * 8 : 8;
-        tn = r / rows;
-        tm = grp * 8 + (r - tn * rows);
-    }
-    const int64_t m0 = int64_t(tm) * TILE;
-    const int64_t n0 = int64_t(tn) * (PROD == kProj ? HALF : TILE);
-    const int all_steps = a.segs * a.steps_seg;
-    const int s_lo = int(int64_t(all_steps) * split / a.splits);
-    const int s_hi = int(int64_t(all_steps) * (split + 1) / a.splits);
-    const int steps = s_hi - s_lo;
-
-    // ---- operand sources ----
-    Operand<AROWS, false, HALF> A;
-    Operand<BROWS, PROD == kProj, HALF> B;
-    A.lanes(wave, lane, a.lda);
-    B.lanes(wave, lane, a.ldb);
-    int seg = 0, sk = s_lo;        // segment and step within it of the next loads
-    int left = steps;              // steps still to load
-    if (PROD == kDx && s_lo >= a.steps_seg) { seg = 1; sk = s_lo - a.steps_seg; }
-    const char* ap = static_cast<const char*>(a.a);
-    auto set_sources = [&]() __attribute__((always_inline)) {
-        const int64_t kk = int64_t(sk) * kBK;
-        if constexpr (AROWS) {
-            const char* e = ap + ((a.m - 1) * a.lda + (PROD == kDx ? 2 * a.fp : a.k)) * 2;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                A.base[h] = ap + ((m0 + h * HALF) * a.lda + (PROD == kDx ? seg * a.fp : 0) + kk) * 2;
-                A.end[h] = e;
-            }
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                A.base[h] = ap + (kk * a.lda + m0 + h * HALF) * 2;
-                A.end[h] = ap + a.k * a.lda * 2;
-            }
-        }
-        if constexpr (PROD == kProj) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const char* w = static_cast<const char*>(h ? a.b1 : a.b0);
-                B.base[h] = w + (n0 * a.ldb + kk) * 2;
-                B.end[h] = w + ((a.n - 1) * a.ldb + a.k) * 2;
-            }
-        } else {
-            const char* w = static_cast<const char*>(PROD == kDx && seg ? a.b1 : a.b0);
-            // rows of the right operand that exist
-            const int64_t rows = PROD == kDx ? a.f : a.k;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                B.base[h] = w + (kk * a.ldb + n0 + h * HALF) * 2;
-                B.end[h] = w + ((rows - 1) * a.ldb + a.nb) * 2;
-            }
-        }
-    };
-    set_sources();
-    auto advance = [&]() __attribute__((always_inline)) {
-        --left;
-        ++sk;
-        if (PROD == kDx && sk == a.steps_seg && seg == 0) {
+    // ---- load cursor ----
+    // Row operands: a view of the tile's rows, the reduction by the loads'
+    // scalar offset.  Reduction operands: a view of a step's 64 rows that moves
+    // on with the cursor, shorter at the end of the operand.
+    const Operand<AROWS, false, HALF> A(wave, lane, a.lda);
+    const Operand<BROWS, PROD == kProj, HALF> B(wave, lane, a.ldb);
+    const char *pa_src = nullptr, *pb_src = nullptr, *pu_src = nullptr;   // view bases (pu_src: PROJ, wu)
+    uint32_t na = 0, nb = 0;       // their lengths
+    uint32_t na_end = 0, nb_end = 0;   // lengths in a segment's last step (reduction operands)
+    uint32_t so = 0;               // bytes into the rows (row operands)
+    uint32_t so_step = kBK * 2;    // 0 once no tile is left: an offset past an empty view would pass its check
+    const int k_end = int(a.k - int64_t(a.steps_seg - 1) * kBK);   // depth of a segment's last step
+    int cv = blockIdx.x;           // tile
+    int seg = 0, sk = 0;           // segment and step within it
+    int todo = 0;                  // steps left of the tile; 0: no tile left, the views are empty
+    auto aim = [&](const Tile& t) __attribute__((always_inline)) {
+        ArgsMem& a = args_again();
+        todo = t.steps;
+        sk = t.s_lo;
+        seg = 0;
+        if (PROD == kDx && sk >= a.steps_seg) {
             seg = 1;
+            sk -= a.steps_seg;
+        }
+        const int64_t kk = int64_t(sk) * kBK;
+        const int64_t ktail = (PROD == kDx ? a.f : a.k) - int64_t(a.steps_seg - 1) * kBK;   // rows of the last step
+        so = uint32_t(kk * 2);
+        const char* ap = static_cast<const char*>(a.a);
+        if constexpr (AROWS) {
+            const int64_t rows = a.m - t.m0 < TILE ? a.m - t.m0 : TILE;
+            pa_src = ap + (t.m0 * a.lda + (PROD == kDx ? seg * a.fp : 0)) * 2;
+            // (in DX the last row of dg ends where its du begins: the mask of
+            // the reduction's end keeps every lane inside)
+            na = uint32_t(((rows - 1) * a.lda + a.k) * 2);
+        } else {
+            pa_src = ap + (kk * a.lda + t.m0) * 2;
+            na = uint32_t(kBK * a.lda * 2);
+            na_end = uint32_t((ktail * a.lda - t.m0) * 2);
+        }
+        if constexpr (BROWS) {
+            const int64_t rows = a.n - t.n0 < HALF ? a.n - t.n0 : HALF;
+            pb_src = static_cast<const char*>(a.b0) + t.n0 * a.ldb * 2;
+            pu_src = static_cast<const char*>(a.b1) + t.n0 * a.ldb * 2;
+            nb = uint32_t(((rows - 1) * a.ldb + a.k) * 2);
+        } else {
+            pb_src = static_cast<const char*>(PROD == kDx && seg ? a.b1 : a.b0) + (kk * a.ldb + t.n0) * 2;
+            nb = uint32_t(kBK * a.ldb * 2);
+            nb_end = uint32_t(((ktail - 1) * a.ldb + a.nb - t.n0) * 2);
+        }
+    };
+    Load la0, la1, lb0, lb1;       // of the cursor's step; la1: of the step before
+    const uint32_t to_a = lds_addr(lds) + wave * 2048, to_b = to_a + BBASE;
+    // (the same in every lane, which the compiler does not always see)
+    auto uni = [](uint32_t v) __attribute__((always_inline)) -> int { return __builtin_amdgcn_readfirstlane(int(v)); };
+    auto rsrc = [&](const char* p, uint32_t n) __attribute__((always_inline)) -> i32x4 {
+        const uint64_t u = reinterpret_cast<uint64_t>(p);
+        return i32x4{uni(uint32_t(u)), uni(uint32_t(u >> 32) & 0xffffu), uni(n), int(kRsrcWord3)};
+    };
+    // the cursor's loads from its state; what they write goes to stage stg
+    auto set_a = [&](Load& l, auto hc, int stg) __attribute__((always_inline)) {
+        constexpr int h = decltype(hc)::value;
+        const bool last = sk == a.steps_seg - 1;
+        l.r = rsrc(pa_src, !AROWS && last ? na_end : na);
+        l.s = AROWS ? uint32_t(uni(so)) : 0u;
+        l.to = to_a + (h * 2 + stg) * HBYTES;
+        const int kl = last ? k_end : kBK;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) l.v[q] = !AROWS || A.lane_k[q] < kl ? A.voff[q] + h * A.half : kOob;
+    };
+    auto set_b = [&](Load& l, auto hc, int stg) __attribute__((always_inline)) {
+        constexpr int h = decltype(hc)::value;
+        const bool last = sk == a.steps_seg - 1;
+        l.r = rsrc(BROWS && h ? pu_src : pb_src, !BROWS && last ? nb_end : nb);
+        l.s = BROWS ? uint32_t(uni(so)) : 0u;
+        l.to = to_b + (h * 2 + stg) * HBYTES;
+        const int kl = last ? k_end : kBK;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            l.v[q] = !BROWS || B.lane_k[q] < kl ? B.voff[q] + (BROWS ? 0 : h * B.half) : kOob;
+    };
+    auto set_all = [&](int stg) __attribute__((always_inline)) {
+        set_a(la0, IC<0>{}, stg);
+        set_b(lb0, IC<0>{}, stg);
+        set_b(lb1, IC<1>{}, stg);
+    };
+    // one step on within the tile
+    auto advance = [&]() __attribute__((always_inline)) {
+        --todo;
+        ++sk;
+        so += so_step;
+        if (!AROWS) pa_src += kBK * a.lda * 2;
+        if (!BROWS) pb_src += kBK * a.ldb * 2;
+    };
+    // past the end of a tile or of a segment
+    auto turn = [&]() __attribute__((always_inline)) {
+        if (todo == 0) {
+            cv += int(gridDim.x);
+            if (cv < total) {
+                aim(tile_of<TILE, NT>(cv));
+            } else {
+                todo = 0x7fffffff;
+                sk = 0;
+                so = so_step = 0;
+                na = nb = na_end = nb_end = 0;
+            }
+        } else if (PROD == kDx && seg == 0 && sk == a.steps_seg) {
+            ArgsMem& a = args_again();
+            seg = 1;   // on to du and wu
             sk = 0;
-        }
-        set_sources();
-    };
-    // the two loads of this wave for one half tile of the cursor's step
-    int akc[2], bkc[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        akc[q] = Operand<AROWS, false, HALF>::lane_k(wave, lane, q);
-        bkc[q] = Operand<BROWS, PROD == kProj, HALF>::lane_k(wave, lane, q);
-    }
-    auto view = [&](const char* base, const char* end) __attribute__((always_inline)) {
-        const int64_t n = left > 0 ? end - base : 0;
-        return make_rsrc(base, n > 0 ? (n < 0x7fffffff ? uint32_t(n) : 0x7fffffffu) : 0u);
-    };
-    auto load_a = [&](auto hc, auto stg) __attribute__((always_inline)) {
-        constexpr int H = decltype(hc)::value, STG = decltype(stg)::value;
-        const __amdgpu_buffer_rsrc_t r = view(A.base[H], A.end[H]);
-        const int64_t kleft = a.k - int64_t(sk) * kBK;
-        const int kl = kleft < kBK ? int(kleft) : kBK;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint32_t vo = !AROWS || akc[q] < kl ? A.voff[q] : kOob;
-            dma16(r, lds + (H * 2 + STG) * HBYTES + (wave * 2 + q) * 1024, vo, 0);
+            so = 0;
+            pa_src += a.fp * 2;
+            pb_src = static_cast<const char*>(a.b1) +
+                        (pb_src - static_cast<const char*>(a.b0) - int64_t(a.steps_seg) * kBK * a.ldb * 2);
         }
     };
-    auto load_b = [&](auto hc, auto stg) __attribute__((always_inline)) {
-        constexpr int H = decltype(hc)::value, STG = decltype(stg)::value;
-        const __amdgpu_buffer_rsrc_t r = view(B.base[H], B.end[H]);
-        const int64_t kleft = a.k - int64_t(sk) * kBK;
-        const int kl = kleft < kBK ? int(kleft) : kBK;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint32_t vo = !BROWS || bkc[q] < kl ? B.voff[q] : kOob;
-            dma16(r, lds + BBASE + (H * 2 + STG) * HBYTES + (wave * 2 + q) * 1024, vo, 0);
-        }
+    auto at_turn = [&]() __attribute__((always_inline)) -> bool {
+        return todo == 0 || (PROD == kDx && seg == 0 && sk == a.steps_seg);
     };
 
-    // ---- fragment addresses ----
+    // ---- fragment addresses, in the stage of the current step ----
     const int fr = lane & 15, grp = lane >> 4;
     const uint32_t lds0 = lds_addr(lds);
-    uint32_t pa[4], pb[2];
+    constexpr int HB = 4 * HALF * 2, KB = 32 * HALF * 2;
+    uint32_t pa[AROWS ? 2 : QM], pb[2];
     if constexpr (AROWS) {
-        const uint32_t row = uint32_t(wm * QM * 16 + fr) * 128;
-        pa[0] = lds0 + row + ((grp ^ (fr & 7)) << 4);
-        pa[1] = lds0 + row + (((grp + 4) ^ (fr & 7)) << 4);
-        pa[2] = pa[3] = 0;
+        const uint32_t row = lds0 + uint32_t(wm * QM * 16 + fr) * 128;
+        pa[0] = row + ((grp ^ (fr & 7)) << 4);
+        pa[1] = row + (((grp + 4) ^ (fr & 7)) << 4);
     } else {
         const int k = grp * 8 + (fr >> 2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            pa[i] = i < QM ? lds0 + k * (HALF * 2) + (((wm * QM + i) ^ Operand<false, false, HALF>::kswz(k)) << 5) +
-                                 8 * (fr & 3)
-                           : 0;
+        for (int i = 0; i < QM; ++i)
+            pa[i] = lds0 + k * (HALF * 2) + (((wm * QM + i) ^ Operand<false, false, HALF>::swz(k)) << 5) + 8 * (fr & 3);
     }
     if constexpr (BROWS) {
-        const uint32_t row = uint32_t(wn * 32 + 8 * (fr >> 2) + (fr & 3)) * 128;
-        pb[0] = lds0 + BBASE + row + ((grp ^ (fr & 7)) << 4);
-        pb[1] = lds0 + BBASE + row + (((grp + 4) ^ (fr & 7)) << 4);
+        const uint32_t row = lds0 + BBASE + uint32_t(wn * 32 + 8 * (fr >> 2) + (fr & 3)) * 128;
+        pb[0] = row + ((grp ^ (fr & 7)) << 4);
+        pb[1] = row + (((grp + 4) ^ (fr & 7)) << 4);
     } else {
         const int k = grp * 8 + (fr >> 2);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            pb[j] = lds0 + BBASE + k * (HALF * 2) + (((wn * 2 + j) ^ Operand<false, false, HALF>::kswz(k)) << 5) +
+            pb[j] = lds0 + BBASE + k * (HALF * 2) + (((wn * 2 + j) ^ Operand<false, false, HALF>::swz(k)) << 5) +
                     8 * (fr & 3);
     }
 
-    i32x4 fa[QM][2], fb0[2][2], fb1[2][2];
+    i32x4 fa[QM][2], fb0[2][2], fb1[2][2], fbn[2][2];   // fbn: column half 0 of the next step
     f32x4 acc[2][2][QM][2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int i = 0; i < QM; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[x][y][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    auto read_a = [&](auto hc, auto stg) __attribute__((always_inline)) {
-        constexpr int OFF = (decltype(hc)::value * 2 + decltype(stg)::value) * HBYTES;
-        if constexpr (AROWS) {
-            read_rows<QM, OFF, 2048>(fa, pa[0], pa[1]);
-        } else {
-            read_cols2<OFF, 32 * HALF * 2, 4 * HALF * 2>(fa[0], fa[1], pa[0], pa[1]);
-            if constexpr (QM == 4)
-                read_cols2<OFF, 32 * HALF * 2, 4 * HALF * 2>(fa[2], fa[3], pa[2], pa[3]);
-        }
-    };
-    auto read_b = [&](i32x4 (&f)[2][2], auto hc, auto stg) __attribute__((always_inline)) {
-        constexpr int OFF = (decltype(hc)::value * 2 + decltype(stg)::value) * HBYTES;
-        if constexpr (BROWS) read_rows<2, OFF, 512>(f, pb[0], pb[1]);
-        else read_cols2<OFF, 32 * HALF * 2, 4 * HALF * 2>(f[0], f[1], pb[0], pb[1]);
-    };
-    auto multiply = [&](auto xc, auto yc) __attribute__((always_inline)) {
+    // products of row half X with column half Y; FIRST: the tile's first, onto 0
+    auto products = [&](auto xc, auto yc, auto fc) __attribute__((always_inline)) {
         constexpr int X = decltype(xc)::value, Y = decltype(yc)::value;
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_barrier();
-        if (PP) __builtin_amdgcn_s_setprio(1);
-        __builtin_amdgcn_sched_barrier(0);
+        constexpr bool FIRST = decltype(fc)::value != 0;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+        for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
             for (int i = 0; i < QM; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    acc[X][Y][i][j] = mfma16x16x32<T>(Y ? fb1[j][ks] : fb0[j][ks], fa[i][ks], acc[X][Y][i][j]);
+                    acc[X][Y][i][j] = mfma16x16x32<T>(Y ? fb1[j][ks] : fb0[j][ks], fa[i][ks],
+                                                      FIRST && ks == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[X][Y][i][j]);
+        }
+    };
+    auto begin = [&]() __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        if (PP) __builtin_amdgcn_s_setprio(1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto end = [&]() __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
         if (PP) {
             __builtin_amdgcn_s_setprio(0);
@@ -347,139 +516,250 @@ __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_k
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    using H0 = IC<0>;
-    using H1 = IC<1>;
-    auto step = [&](auto stg) __attribute__((always_inline)) {
-        using S = decltype(stg);
-        using N = IC<1 - S::value>;
-        load_b(H0{}, S{});
-        read_a(H0{}, S{});
-        wait_vm<12>();
-        multiply(H0{}, H0{});
-        load_a(H0{}, S{});
-        read_b(fb1, H1{}, S{});
-        wait_vm<12>();
-        multiply(H0{}, H1{});
-        load_b(H1{}, S{});
-        read_a(H1{}, S{});
-        wait_vm<12>();
-        multiply(H1{}, H1{});
-        load_a(H1{}, S{});
+    int par = 0;                   // stage of the current step
+    int delta = HBYTES;            // to the other stage's fragments
+    bool drained = true;           // no result stores behind the loads in flight
+    auto step = [&](auto fc) __attribute__((always_inline)) {
+        constexpr bool FIRST = decltype(fc)::value != 0;
+        auto wait = [&]() __attribute__((always_inline)) {
+            if (FIRST && STORES > 0 && !drained) wait_vm<8 + STORES>();
+            else wait_vm<8>();
+        };
+        // phase 0; loads row half 1 of the next step, column half 0 of the one after
+        if constexpr (BROWS) read_rows_rows<0, 2 * HBYTES>(fa, fb1, pa, pb, la1, lb0);
+        else if constexpr (AROWS) read_rows_cols<0, 2 * HBYTES, HB, KB>(fa, fb1, pa, pb, la1, lb0);
+        else read_cols_cols<0, 2 * HBYTES, HB, KB>(fa, fb1, pa, pb, la1, lb0);
+        wait();
+        begin();
+        products(IC<0>{}, IC<0>{}, fc);
+        products(IC<0>{}, IC<1>{}, fc);
+        end();
+        // phase 1; loads row half 0 and column half 1 of the step after next
+        {
+            const uint32_t pn[2] = {pb[0] + delta, pb[1] + delta};
+            if constexpr (BROWS) read_rows_rows<2 * HBYTES, 0>(fa, fbn, pa, pn, la0, lb1);
+            else if constexpr (AROWS) read_rows_cols<2 * HBYTES, 0, HB, KB>(fa, fbn, pa, pn, la0, lb1);
+            else read_cols_cols<2 * HBYTES, 0, HB, KB>(fa, fbn, pa, pn, la0, lb1);
+        }
+        wait();
+        begin();
+        products(IC<1>{}, IC<0>{}, fc);
+        products(IC<1>{}, IC<1>{}, fc);
+        // between them: the cursor's next loads (for now as if the tile went
+        // on, so that no branch parts them from the products) and the other
+        // stage's addresses
+        set_a(la1, IC<1>{}, par);
         advance();
-        // fb0 of this step is still to be multiplied: the next step's goes
-        // to a copy that takes its place afterwards
-        i32x4 next[2][2];
-        read_b(next, H0{}, N{});
-        wait_vm<12>();
-        multiply(H1{}, H0{});
+        par ^= 1;
+        set_all(par);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) fb0[j][ks] = next[j][ks];
+            for (int ks = 0; ks < 2; ++ks) fb0[j][ks] = fbn[j][ks];
+#pragma unroll
+        for (int i = 0; i < (AROWS ? 2 : QM); ++i) pa[i] += delta;
+        pb[0] += delta;
+        pb[1] += delta;
+        delta = -delta;
+#pragma unroll
+        for (int i = 0; i < 4 * QM; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, QM == 4 ? 2 : 1, 0);   // products
+            __builtin_amdgcn_sched_group_barrier(0x004, 3, 0);                 // scalar
+            __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);                 // vector
+        }
+        if (at_turn()) {
+            turn();
+            set_all(par);
+        }
+        end();
     };
 
-    // ---- prologue: two steps of loads, the first column half ----
-    load_b(H0{}, IC<0>{});
-    load_a(H0{}, IC<0>{});
-    load_b(H1{}, IC<0>{});
-    load_a(H1{}, IC<0>{});
-    advance();
-    load_b(H0{}, IC<1>{});
-    load_a(H0{}, IC<1>{});
-    load_b(H1{}, IC<1>{});
-    load_a(H1{}, IC<1>{});
-    advance();
-    wait_vm<12>();
-    __builtin_amdgcn_s_barrier();
-    read_b(fb0, H0{}, IC<0>{});
-    __builtin_amdgcn_s_barrier();
-    if (PP && wm == 1) __builtin_amdgcn_s_barrier();
-    for (int s = 0; s < steps; s += 2) {
-        step(IC<0>{});
-        if (s + 1 < steps) step(IC<1>{});
-    }
-    if (PP && wm == 0) __builtin_amdgcn_s_barrier();
-    wait_vm<0>();   // the loads past the last step still write LDS
-
-    // ---- results ----
-    if constexpr (PROD == kProj) {
-        const int64_t f = n0 + wn * 32 + 8 * grp;   // 8 hidden units per lane
-        if (f >= a.fp) return;
+    // ---- results of a tile ----
+    // (the views' bases and lengths cover the rows of this tile; an offset of
+    // kOob is dropped)
+    auto results = [&](const Tile& t) __attribute__((always_inline)) {
+        ArgsMem& a = args_again();
+        int mrow = wm * QM * 16 + fr;                 // + half * HALF + 16 * i
+        asm volatile("" : "+v"(mrow));                // offsets are not worth registers over the steps
+        const int64_t mleft = a.m - t.m0;
+        bool wide = a.wide != 0;   // whole 16-byte vectors, all inside or all outside the result
+        if constexpr (END == kEndPart) {
+            constexpr int64_t HSTEP = PROD == kProj ? 0 : HALF;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int i = 0; i < QM; ++i) {
-                const int64_t m = m0 + x * HALF + (wm * QM + i) * 16 + fr;
-                if (m >= a.m) continue;
-                if constexpr (END == kEndPart) {
-                    float* p = a.part + (int64_t(split) * a.m + m) * a.part_ld + f;
+                for (int i = 0; i < QM; ++i) {
+                    const int64_t ml = x * HALF + mrow + 16 * i;
+                    if (ml >= mleft) continue;
+                    float* p = a.part + (int64_t(t.split) * a.m + t.m0 + ml) * a.part_ld;
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            *reinterpret_cast<f32x4*>(p + y * a.fp + 4 * j) = acc[x][y][i][j];
-                } else if constexpr (END == kEndFwd) {
-                    float o[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[e] = act_value(ACT, acc[x][0][i][e >> 2][e & 3]) * acc[x][1][i][e >> 2][e & 3];
-                    store_n<T>(static_cast<char*>(a.y) + (m * a.ldy + f) * 2, pack_vec<T>(o), int(a.f - f < 8 ? a.f - f : 8));
-                } else {
-                    const int left = int(a.f - f < 8 ? a.f - f : 8);
-                    const i32x4 dyv = load_n<T>(static_cast<const char*>(a.dy) + (m * a.lddy + f) * 2, left);
-                    float dg[8], du[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float v, d;
-                        act_both(ACT, acc[x][0][i][e >> 2][e & 3], v, d);
-                        const float t = elem<T>(dyv, e);
-                        // the columns f..fp-1 are operands of dx: exactly 0
-                        dg[e] = e < left ? t * acc[x][1][i][e >> 2][e & 3] * d : 0.0f;
-                        du[e] = e < left ? t * v : 0.0f;
-                    }
-                    char* p = static_cast<char*>(a.dgu) + (m * 2 * a.fp + f) * 2;
-                    *reinterpret_cast<i32x4*>(p) = pack_vec<T>(dg);
-                    *reinterpret_cast<i32x4*>(p + a.fp * 2) = pack_vec<T>(du);
-                }
-            }
-    } else {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int i = 0; i < QM; ++i) {
-                const int64_t m = m0 + x * HALF + (wm * QM + i) * 16 + fr;
-                if (m >= a.m) continue;
-                char* row = nullptr;
-                if constexpr (END != kEndPart) {
-                    if constexpr (PROD == kDx) {
-                        row = static_cast<char*>(a.y) + m * a.ldy * 2;
-                    } else {
-                        const bool up = m >= a.fp;
-                        const int64_t f = up ? m - a.fp : m;
-                        if (f >= a.f) continue;
-                        row = static_cast<char*>(up ? a.dwu : a.dwg) + f * a.n * 2;
-                    }
-                }
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int64_t n = n0 + y * HALF + wn * 32 + j * 16 + 4 * grp;
-                        const f32x4 v = acc[x][y][i][j];
-                        if (n >= a.n) continue;
-                        if constexpr (END == kEndPart) {
-                            *reinterpret_cast<f32x4*>(a.part + (int64_t(split) * a.m + m) * a.part_ld + n) = v;
-                        } else if (n + 4 <= a.n) {
-                            struct __attribute__((packed, aligned(2))) W2 { uint32_t w[2]; };
-                            *reinterpret_cast<W2*>(row + n * 2) = W2{{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])}};
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 3; ++e)
-                                if (n + e < a.n) store1<T>(row + (n + e) * 2, v[e]);
+                        for (int j = 0; j < 2; ++j) {
+                            // PROJ: 8 hidden units a lane over its two tiles
+                            const int64_t n = t.n0 + y * HSTEP + wn * 32 +
+                                              (PROD == kProj ? 8 * grp + 4 * j : 16 * j + 4 * grp);
+                            if (n < (PROD == kProj ? a.fp : a.n))
+                                *reinterpret_cast<f32x4*>(p + (PROD == kProj ? y * a.fp : 0) + n) = acc[x][y][i][j];
                         }
+                }
+        } else if constexpr (PROD == kProj) {
+            const int fl = wn * 32 + 8 * grp;         // 8 hidden units a lane
+            const int64_t f = t.n0 + fl;
+            const int cnt = int(a.f - f < 8 ? a.f - f : 8);   // that exist
+            if constexpr (END == kEndFwd) {
+                char* yp = static_cast<char*>(a.y) + (t.m0 * a.ldy + t.n0) * 2;
+                const __amdgpu_buffer_rsrc_t ry = view(yp, ((mleft - 1) * a.ldy + a.f - t.n0) * 2);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < QM; ++i) {
+                        float o[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[e] = act_value(ACT, acc[x][0][i][e >> 2][e & 3]) * acc[x][1][i][e >> 2][e & 3];
+                        const int ml = x * HALF + mrow + 16 * i;
+                        const i32x4 v = pack_vec<T>(o);
+                        if (wide)
+                            store16_at(v, ry, cnt == 8 && ml < mleft ? uint32_t((ml * a.ldy + fl) * 2) : kOob);
+                        else if (ml < mleft)
+                            store_n<T>(yp + (ml * a.ldy + fl) * 2, v, cnt);
+                    }
+            } else {
+                const char* dp = static_cast<const char*>(a.dy) + (t.m0 * a.lddy + t.n0) * 2;
+                const __amdgpu_buffer_rsrc_t rd = view(dp, ((mleft - 1) * a.lddy + a.f - t.n0) * 2);
+                char* gp = static_cast<char*>(a.dgu) + (t.m0 * 2 * a.fp + t.n0) * 2;
+                const __amdgpu_buffer_rsrc_t rg = view(gp, (mleft * 2 * a.fp - t.n0) * 2);
+                i32x4 dyv[2][QM];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < QM; ++i) {
+                        const int ml = x * HALF + mrow + 16 * i;
+                        if (wide)
+                            dyv[x][i] = buf_load16(rd, cnt == 8 && ml < mleft ? uint32_t((ml * a.lddy + fl) * 2) : kOob);
+                        else
+                            dyv[x][i] = load_n<T>(dp + (ml * int64_t(a.lddy) + fl) * 2, ml < mleft ? cnt : 0);
+                    }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < QM; ++i) {
+                        float dg[8], du[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float v, d;
+                            act_both(ACT, acc[x][0][i][e >> 2][e & 3], v, d);
+                            const float t1 = elem<T>(dyv[x][i], e);
+                            // the columns f..fp-1 are operands of dx: exactly 0
+                            dg[e] = e < cnt ? t1 * acc[x][1][i][e >> 2][e & 3] * d : 0.0f;
+                            du[e] = e < cnt ? t1 * v : 0.0f;
+                        }
+                        const int ml = x * HALF + mrow + 16 * i;
+                        const uint32_t o = f < a.fp && ml < mleft ? uint32_t((ml * 2 * a.fp + fl) * 2) : kOob;
+                        store16_at(pack_vec<T>(dg), rg, o);
+                        store16_at(pack_vec<T>(du), rg, o == kOob ? kOob : o + uint32_t(a.fp * 2));
                     }
             }
+        } else {
+            // rows of dx, or of dwg and then dwu; a tile of DW that holds the
+            // last rows of dwg and the first of dwu goes the narrow way
+            const bool up = PROD == kDw && t.m0 >= a.fp;
+            const int64_t r0 = up ? t.m0 - a.fp : t.m0;
+            const int64_t ld = PROD == kDw ? a.n : a.ldy;
+            const int64_t rows = PROD == kDw ? a.f - r0 : mleft;
+            char* op = static_cast<char*>(PROD == kDx ? a.y : up ? a.dwu : a.dwg) + (r0 * ld + t.n0) * 2;
+            wide = wide && (PROD == kDx || up || t.m0 + TILE <= a.fp);
+            if (wide) {
+                const __amdgpu_buffer_rsrc_t ro = view(op, ((rows - 1) * ld + a.n - t.n0) * 2);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < QM; ++i)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            // lanes of odd 16-lane rows take the second tile: 8 consecutive columns each
+                            const f32x4 v0 = acc[x][y][i][0], v1 = acc[x][y][i][1];
+                            const auto lo = __builtin_amdgcn_permlane16_swap(pack2<T>(v0[0], v0[1]),
+                                                                             pack2<T>(v1[0], v1[1]), false, false);
+                            const auto hi = __builtin_amdgcn_permlane16_swap(pack2<T>(v0[2], v0[3]),
+                                                                             pack2<T>(v1[2], v1[3]), false, false);
+                            const int ml = x * HALF + mrow + 16 * i;
+                            const int c = y * HALF + wn * 32 + 16 * (grp & 1) + 8 * (grp >> 1);
+                            store16_at(i32x4{int(lo[0]), int(hi[0]), int(lo[1]), int(hi[1])}, ro,
+                                       ml < rows && t.n0 + c < a.n ? uint32_t((ml * ld + c) * 2) : kOob);
+                        }
+            } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < QM; ++i) {
+                        const int ml = x * HALF + mrow + 16 * i;
+                        char* row = op + ml * ld * 2;
+                        bool in = ml < mleft;
+                        if constexpr (PROD == kDw) {
+                            const int64_t m = t.m0 + ml, f = m >= a.fp ? m - a.fp : m;
+                            in = in && f < a.f;
+                            row = static_cast<char*>(m >= a.fp ? a.dwu : a.dwg) + (f * ld + t.n0) * 2;
+                        }
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int c = y * HALF + wn * 32 + 16 * j + 4 * grp;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (in && t.n0 + c + e < a.n) store1<T>(row + (c + e) * 2, acc[x][y][i][j][e]);
+                            }
+                    }
+            }
+        }
+        drained = !wide || STORES == 0;
+        if (drained) wait_vm<0>();
+    };
+
+    // ---- the block's tiles ----
+    Tile cur = tile_of<TILE, NT>(int(blockIdx.x));
+    aim(cur);
+    // steps 0 and 1 but for row half 1 of step 1, which phase 0 loads
+    auto load = [&](const Load& l) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(
+            reinterpret_cast<const void*>(uint64_t(uint32_t(l.r[0])) | uint64_t(uint32_t(l.r[1])) << 32), uint32_t(l.r[2]));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) dma16(r, lds + (l.to - lds_addr(lds)) + q * 1024, l.v[q], l.s);
+    };
+    set_all(0);
+    load(lb0);
+    load(la0);
+    load(lb1);
+    set_a(la1, IC<1>{}, 0);
+    load(la1);
+    advance();
+    if (at_turn()) turn();
+    set_all(1);
+    load(lb0);
+    load(la0);
+    load(lb1);
+    set_a(la1, IC<1>{}, 1);
+    advance();
+    if (at_turn()) turn();
+    set_all(0);
+    wait_vm<8>();
+    __builtin_amdgcn_s_barrier();
+    if constexpr (BROWS) read_rows<0>(fb0, pb);
+    else read_cols<0, HB, KB>(fb0, pb);
+    __builtin_amdgcn_s_barrier();
+    if (PP && wm == 1) __builtin_amdgcn_s_barrier();
+    for (int v = blockIdx.x;;) {
+        step(IC<1>{});
+        for (int s = 1; s < cur.steps; ++s) step(IC<0>{});
+        results(cur);
+        v += int(gridDim.x);
+        if (v >= total) break;
+        cur = tile_of<TILE, NT>(v);
     }
+    if (PP && wm == 0) __builtin_amdgcn_s_barrier();
+    wait_vm<0>();   // the loads past the last step still write LDS
 }
 
 // ---- joining a split reduction: splits are added in ascending order -------------
@@ -573,8 +853,11 @@ unsigned blocks_for(int64_t n) {
 
 template <typename T, int PROD, int END, int ACT>
 int launch_tile(int tile, const GatedArgs& a, hipStream_t st) {
-    const int64_t blocks = int64_t(a.tiles_m) * a.tiles_n * a.splits;
-    if (blocks < 1 || blocks > 0x7fffffff) return CNHWC_UNSUPPORTED;
+    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n * a.splits;
+    // (block indices run past the last tile by at most one grid)
+    if (tiles < 1 || tiles > 0x7fffffff - 4 * kNumCUs) return CNHWC_UNSUPPORTED;
+    const int64_t slots = tile == kGatedBig ? kNumCUs : 2 * kNumCUs;
+    const int64_t blocks = tiles < slots ? tiles : slots;
     if (tile == kGatedBig)
         gated_gemm_kernel<T, PROD, kGatedBig, END, ACT><<<dim3((unsigned)blocks), 512, 0, st>>>(a);
     else

@@ -374,6 +374,7 @@ int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const voi
     a.lddy = p.ys;
     a.dgu = bwd ? w + g.off_dgu : nullptr;
     a.part_ld = 2 * g.fp;
+    a.wide = p.f % 8 == 0 && p.ys % 8 == 0 && !off16(bwd ? dy : y);
     if ((rc = run_product(p.dtype, kProj, g.proj, a, w, g.off_part, st))) return rc;
     if (dx) {
         GatedArgs d = a;
@@ -387,6 +388,7 @@ int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const voi
         d.y = dx;
         d.ldy = p.xs;
         d.part_ld = up(p.c, 4);
+        d.wide = p.c % 8 == 0 && p.xs % 8 == 0 && !off16(dx);
         if ((rc = run_product(p.dtype, kDx, g.dx, d, w, g.off_part, st))) return rc;
     }
     if (dwg) {
@@ -404,6 +406,7 @@ int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const voi
         d.dwg = dwg;
         d.dwu = dwu;
         d.part_ld = up(p.c, 4);
+        d.wide = p.c % 8 == 0 && !off16(dwg) && !off16(dwu);
         if ((rc = run_product(p.dtype, kDw, g.dw, d, w, g.off_part, st))) return rc;
     }
     return ok();

@@ -12,6 +12,7 @@ been built: there is no fallback.
 """
 import contextlib
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -187,11 +188,13 @@ def cnhwc_wgrad(p, x, dy, dw, ws, ws_bytes, stream):
 
 
 def cnhwc_set_override(variant=0, cpl=0, split_c=0, chunk_limit_bytes=0, tune=0):
+    _gated_desc.cache_clear()
     _check(lib().cnhwc_set_override(ctypes.byref(Override(variant, cpl, split_c, tune,
                                                           chunk_limit_bytes))))
 
 
 def cnhwc_clear_override():
+    _gated_desc.cache_clear()
     _check(lib().cnhwc_set_override(None))
 
 
@@ -270,39 +273,47 @@ def wgrad(x, dy, p, dw=None, ws=None):
 # x's device; a tensor written on another stream has to be waited for first, as
 # in PyTorch.
 
-def _mix_dtype(torch, t, what, f32=True):
-    kinds = {torch.float16: F16, torch.bfloat16: BF16}
-    if f32:
-        kinds[torch.float32] = F32
-    if t.dtype not in kinds:
-        raise ValueError("%s must be %s (got %s)" % (
-            what, ", ".join(str(k) for k in kinds), t.dtype))
-    return kinds[t.dtype]
+_torch = None
+_mix_types = {}
+
+
+def _t():
+    """PyTorch, imported on first use, and the element types by torch dtype."""
+    global _torch
+    if _torch is None:
+        import torch
+        _mix_types.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+        _torch = torch
+    return _torch
 
 
 def _rows(t, what, width=None):
     """(rows, width, row stride) of a tensor seen as rows of its last dimension."""
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError("%s needs at least one dimension" % what)
-    c = t.shape[-1]
+    c = shape[-1]
     if width is not None and c != width:
         raise ValueError("%s has %d channels, expected %d" % (what, c, width))
+    n = t.numel()
+    if n and t.is_contiguous():
+        return n // c, c, c
     rows = 1
-    for s in t.shape[:-1]:
+    for s in shape[:-1]:
         rows *= s
-    if rows == 0 or c == 0:
+    if not n:
         return rows, c, c
     if t.stride(-1) != 1 and c > 1:
         raise ValueError("%s: channels are not contiguous" % what)
     stride, inner = None, 1      # walk outwards; dimensions of size 1 have no step
-    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if stride is None:
             stride = st
         elif st != stride * inner:
             raise ValueError("%s: its leading dimensions do not step evenly (shape %s, strides %s)"
-                             % (what, tuple(t.shape), tuple(t.stride())))
+                             % (what, tuple(shape), tuple(t.stride())))
         inner *= size
     if stride is None:
         stride = c
@@ -318,91 +329,127 @@ def _same(t, ref, what, dtype=None):
         raise ValueError("%s is %s, expected %s" % (what, t.dtype, dtype or ref.dtype))
 
 
-def _on_gpu(t, what):
-    if t.device.type != "cuda":
+def _operand(t, what, f32=True):
+    """Element type of a GPU tensor."""
+    if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor (got %s)" % (what, t.device))
+    dt = _mix_types.get(t.dtype, -1)
+    if dt < 0 or (dt == F32 and not f32):
+        raise ValueError("%s must be float16, bfloat16%s (got %s)" % (what, " or float32" if f32 else "", t.dtype))
+    return dt
 
 
-def _like_rows(t, shape, what, rows, width, ref, dtype=None):
-    """Row stride of an output given by the caller, or a new dense one."""
-    import torch
+def _out(t, shape, what, rows, width, ref):
+    """(output, its row stride): the caller's, or a new dense one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype or ref.dtype, device=ref.device), width
-    _same(t, ref, what, dtype)
+        return _torch.empty(shape, dtype=ref.dtype, device=ref.device), width
+    _same(t, ref, what)
     r, _, st = _rows(t, what, width)
     if r != rows:
         raise ValueError("%s has %d rows, expected %d" % (what, r, rows))
     return t, st
 
 
-def _vector(t, n, what, ref, dtype):
-    if t is None:
-        return None
-    _same(t, ref, what, dtype)
-    if tuple(t.shape) != (n,) or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous [%d] tensor (got %s)" % (what, n, tuple(t.shape)))
-    return t
+def _vector(t, n, what, ref):
+    """Element type of a per-channel vector."""
+    if t.device != ref.device:
+        raise ValueError("%s is on %s, expected %s" % (what, t.device, ref.device))
+    dt = _mix_types.get(t.dtype, -1)
+    if dt < 0 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous [%d] tensor of float16, bfloat16 or float32 (got %s, %s)"
+                         % (what, n, tuple(t.shape), t.dtype))
+    return dt
 
 
 def _ptr(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return (t.data_ptr() or None) if t is not None else None
 
 
-def _ws(torch, ws, need, device):
+def _ws(ws, need, device):
     """(tensor to keep alive, pointer, bytes) of a workspace of `need` bytes."""
     if ws is None:
         if not need:
             return None, None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _torch.empty(need, dtype=_torch.uint8, device=device)
     elif ws.device != device or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on %s" % device)
     return ws, _ptr(ws), ws.numel() * ws.element_size()
 
 
-def _ln_problem(torch, x, gamma, beta, eps, c, rows, xs, ys):
-    dt = _mix_dtype(torch, x, "x")
+def _enqueue(fn, device, *args):
+    """fn(*args, current stream of device), with device current."""
+    i = device.index
+    if i == _torch.cuda.current_device():
+        _check(fn(*args, _torch._C._cuda_getCurrentRawStream(i)))
+    else:
+        with _torch.cuda.device(device):
+            _check(fn(*args, _torch._C._cuda_getCurrentRawStream(i)))
+
+
+# Descriptors and workspace sizes by their fields (a model calls few shapes
+# often); dropped when the test override changes, which sizes depend on.
+
+@functools.lru_cache(maxsize=1024)
+def _ln_desc(*fields):
+    """(descriptor reference, workspace bytes of the backward pass)"""
+    prob = LayernormProblem(*fields, 0)
+    b = ctypes.c_size_t()
+    _check(lib().cnhwc_layernorm_workspace_size(ctypes.byref(prob), ctypes.byref(b)))
+    return ctypes.byref(prob), b.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_desc(op, unaligned, *fields):
+    """(descriptor reference, workspace bytes)"""
+    prob = GatedProblem(*fields, 0)
+    b = ctypes.c_size_t()
+    _check(lib().cnhwc_gated_workspace_size(ctypes.byref(prob), op, unaligned, ctypes.byref(b)))
+    return ctypes.byref(prob), b.value
+
+
+def _ln_params(dt, gamma, beta, c, ref):
+    """param_dtype of gamma and beta (x's without either)."""
     pd = dt
-    for t, what in ((gamma, "gamma"), (beta, "beta")):
-        if t is not None:
-            pd = _mix_dtype(torch, t, what)
-            _vector(t, c, what, x, t.dtype)
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise ValueError("gamma is %s and beta is %s" % (gamma.dtype, beta.dtype))
-    return LayernormProblem(rows, c, xs, ys, eps, dt, pd, 0)
+    if gamma is not None:
+        pd = _vector(gamma, c, "gamma", ref)
+    if beta is not None:
+        bd = _vector(beta, c, "beta", ref)
+        if gamma is not None and bd != pd:
+            raise ValueError("gamma is %s and beta is %s" % (gamma.dtype, beta.dtype))
+        pd = bd
+    return pd
 
 
 def layernorm(x, gamma=None, beta=None, eps=1e-5, y=None):
     """(y, mean, rstd): layer norm of x [..., c] over its channels, and each
     row's fp32 statistics for layernorm_bwd."""
-    import torch
-    _on_gpu(x, "x")
+    torch = _t()
+    dt = _operand(x, "x")
     rows, c, xs = _rows(x, "x")
-    y, ys = _like_rows(y, x.shape, "y", rows, c, x)
-    prob = _ln_problem(torch, x, gamma, beta, eps, c, rows, xs, ys)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
-    with torch.cuda.device(x.device):
-        _check(lib().cnhwc_layernorm_fwd(ctypes.byref(prob), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y),
-                                         _ptr(mean), _ptr(rstd), _stream_handle(torch, x.device)))
+    pd = _ln_params(dt, gamma, beta, c, x)
+    y, ys = _out(y, x.shape, "y", rows, c, x)
+    prob, _ = _ln_desc(rows, c, xs, ys, eps, dt, pd)
+    dev = x.device
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _enqueue(lib().cnhwc_layernorm_fwd, dev, prob, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
 
 def layernorm_workspace(x, gamma=None):
     """Workspace bytes of layernorm_bwd for this x."""
-    import torch
+    _t()
+    dt = _operand(x, "x")
     rows, c, xs = _rows(x, "x")
-    b = ctypes.c_size_t()
-    prob = _ln_problem(torch, x, gamma, None, 0.0, c, rows, xs, 0)
-    _check(lib().cnhwc_layernorm_workspace_size(ctypes.byref(prob), ctypes.byref(b)))
-    return b.value
+    return _ln_desc(rows, c, xs, 0, 0.0, dt, _ln_params(dt, gamma, None, c, x))[1]
 
 
 def layernorm_bwd(dy, x, mean, rstd, gamma=None, dx=None, param_dtype=None, ws=None):
     """(dx, dgamma, dbeta) of layernorm, from its x and statistics.  dgamma and
-    dbeta have gamma's type (param_dtype, or x's, without a gamma).  dx, if
-    given, has x's row stride."""
-    import torch
-    _on_gpu(x, "x")
+    dbeta have gamma's type (param_dtype, or x's, without a gamma).  dx has x's
+    row stride."""
+    torch = _t()
+    dt = _operand(x, "x")
     rows, c, xs = _rows(x, "x")
     _same(dy, x, "dy")
     drows, _, ys = _rows(dy, "dy", c)
@@ -412,46 +459,41 @@ def layernorm_bwd(dy, x, mean, rstd, gamma=None, dx=None, param_dtype=None, ws=N
         _same(t, x, what, torch.float32)
         if t.numel() != rows or not t.is_contiguous():
             raise ValueError("%s must be a contiguous tensor of %d values" % (what, rows))
-    prob = _ln_problem(torch, x, gamma, None, 0.0, c, rows, xs, ys)
-    pd = gamma.dtype if gamma is not None else (param_dtype or x.dtype)
-    if param_dtype is not None and param_dtype != pd:
-        raise ValueError("param_dtype is %s, gamma is %s" % (param_dtype, pd))
-    prob.param_dtype = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(pd, -1)
+    ptype = gamma.dtype if gamma is not None else (param_dtype or x.dtype)
+    if param_dtype is not None and param_dtype != ptype:
+        raise ValueError("param_dtype is %s, gamma is %s" % (param_dtype, ptype))
+    pd = _ln_params(dt, gamma, None, c, x) if gamma is not None else _mix_types.get(ptype, -1)
     if dx is None:
-        dx = _new_rows(torch, x.shape, xs, x)
+        dx = _new_rows(x.shape, xs, x)
     else:
         _same(dx, x, "dx")
         if _rows(dx, "dx", c)[::2] != (rows, xs):
             raise ValueError("dx must have x's rows and row stride (%d)" % xs)
-    dgamma = torch.empty(c, dtype=pd, device=x.device)
-    dbeta = torch.empty_like(dgamma)
-    need = ctypes.c_size_t()
-    _check(lib().cnhwc_layernorm_workspace_size(ctypes.byref(prob), ctypes.byref(need)))
-    ws, wp, wb = _ws(torch, ws, need.value, x.device)
-    with torch.cuda.device(x.device):
-        _check(lib().cnhwc_layernorm_bwd(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd),
-                                         _ptr(dx), _ptr(dgamma), _ptr(dbeta), wp, wb,
-                                         _stream_handle(torch, x.device)))
+    dev = x.device
+    dgamma = torch.empty(c, dtype=ptype, device=dev)
+    dbeta = torch.empty(c, dtype=ptype, device=dev)
+    prob, need = _ln_desc(rows, c, xs, ys, 0.0, dt, pd)
+    ws, wp, wb = _ws(ws, need, dev)
+    _enqueue(lib().cnhwc_layernorm_bwd, dev, prob, _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
+             _ptr(dgamma), _ptr(dbeta), wp, wb)
     return dx, dgamma, dbeta
 
 
-def _new_rows(torch, shape, stride, ref):
+def _new_rows(shape, stride, ref):
     """A new tensor of `shape` with the given row stride (the entry points give
     dx the row stride of x)."""
     c = shape[-1]
-    rows = 1
-    for s in shape[:-1]:
-        rows *= s
-    if stride == c or rows == 0:
-        return torch.empty(shape, dtype=ref.dtype, device=ref.device)
-    return torch.empty((*shape[:-1], stride), dtype=ref.dtype, device=ref.device)[..., :c]
+    if stride == c:
+        return _torch.empty(shape, dtype=ref.dtype, device=ref.device)
+    return _torch.empty((*shape[:-1], stride), dtype=ref.dtype, device=ref.device)[..., :c]
 
 
-def _gated_problem(torch, x, wg, wu, act, ys=0):
-    _on_gpu(x, "x")
+def _gated_operands(x, wg, wu, act):
+    """(rows, c, f, row stride of x, act, dtype)"""
+    dt = _operand(x, "x", f32=False)
     rows, c, xs = _rows(x, "x")
-    dt = _mix_dtype(torch, x, "x", f32=False)
-    if act not in ACTS:
+    a = ACTS.get(act, -1)
+    if a < 0:
         raise ValueError("act must be one of %s (got %r)" % (", ".join(ACTS), act))
     f = wg.shape[0]
     for w, what in ((wg, "wg"), (wu, "wu")):
@@ -459,70 +501,64 @@ def _gated_problem(torch, x, wg, wu, act, ys=0):
         # [f, c], or the [f, 1, 1, c] filter of a pointwise convolution
         if w.dim() < 2 or w.shape[0] != f or w.shape[-1] != c or w.numel() != f * c or not w.is_contiguous():
             raise ValueError("%s must be a contiguous [%d, %d] tensor (got %s)" % (what, f, c, tuple(w.shape)))
-    return GatedProblem(rows, c, f, xs, ys, ACTS[act], dt, 0)
-
-
-def _gated_need(prob, op, unaligned):
-    b = ctypes.c_size_t()
-    _check(lib().cnhwc_gated_workspace_size(ctypes.byref(prob), op, int(unaligned), ctypes.byref(b)))
-    return b.value
+    return rows, c, f, xs, a, dt
 
 
 def _off16(*tensors):
-    return any(t.data_ptr() % 16 for t in tensors)
+    for t in tensors:
+        if t.data_ptr() & 15:
+            return 1
+    return 0
 
 
 def gated_workspace(x, wg, which="fwd"):
     """Workspace bytes of gated (which="fwd") or gated_bwd ("bwd") for operands
     like x and wg."""
-    import torch
+    _t()
     if which not in ("fwd", "bwd"):
         raise ValueError('which must be "fwd" or "bwd" (got %r)' % (which,))
-    prob = _gated_problem(torch, x, wg, wg, "silu")
-    return _gated_need(prob, OP_FWD if which == "fwd" else OP_DGRAD, _off16(x, wg))
+    rows, c, f, xs, a, dt = _gated_operands(x, wg, wg, "silu")
+    return _gated_desc(OP_FWD if which == "fwd" else OP_DGRAD, _off16(x, wg), rows, c, f, xs, 0, a, dt)[1]
 
 
 def gated_plan(x, wg, which="fwd"):
     """Names of the kernels the call runs on 16-byte-aligned operands."""
-    import torch
-    prob = _gated_problem(torch, x, wg, wg, "silu")
+    _t()
+    rows, c, f, xs, a, dt = _gated_operands(x, wg, wg, "silu")
     buf = ctypes.create_string_buffer(256)
-    _check(lib().cnhwc_gated_plan(ctypes.byref(prob), OP_FWD if which == "fwd" else OP_DGRAD, buf, 256))
+    _check(lib().cnhwc_gated_plan(ctypes.byref(GatedProblem(rows, c, f, xs, 0, a, dt, 0)),
+                                  OP_FWD if which == "fwd" else OP_DGRAD, buf, 256))
     return buf.value.decode()
 
 
 def gated(x, wg, wu, act="silu", y=None, ws=None):
     """act(x wg^T) * (x wu^T) of x [..., c] and wg, wu [f, c] (or [f, 1, 1, c])."""
-    import torch
-    prob = _gated_problem(torch, x, wg, wu, act)
-    y, prob.y_stride = _like_rows(y, (*x.shape[:-1], prob.f), "y", prob.rows, prob.f, x)
-    need = _gated_need(prob, OP_FWD, _off16(x, wg, wu))
-    ws, wp, wb = _ws(torch, ws, need, x.device)
-    with torch.cuda.device(x.device):
-        _check(lib().cnhwc_gated_fwd(ctypes.byref(prob), _ptr(x), _ptr(wg), _ptr(wu), _ptr(y), wp, wb,
-                                     _stream_handle(torch, x.device)))
+    _t()
+    rows, c, f, xs, a, dt = _gated_operands(x, wg, wu, act)
+    y, ys = _out(y, (*x.shape[:-1], f), "y", rows, f, x)
+    prob, need = _gated_desc(OP_FWD, _off16(x, wg, wu), rows, c, f, xs, ys, a, dt)
+    ws, wp, wb = _ws(ws, need, x.device)
+    _enqueue(lib().cnhwc_gated_fwd, x.device, prob, _ptr(x), _ptr(wg), _ptr(wu), _ptr(y), wp, wb)
     return y
 
 
 def gated_bwd(dy, x, wg, wu, act="silu", need_dx=True, need_dw=True, ws=None):
     """(dx, dwg, dwu) of gated; None in the place of what is not needed.  dx
     has x's row stride."""
-    import torch
-    prob = _gated_problem(torch, x, wg, wu, act)
+    torch = _t()
+    rows, c, f, xs, a, dt = _gated_operands(x, wg, wu, act)
     _same(dy, x, "dy")
-    drows, _, prob.y_stride = _rows(dy, "dy", prob.f)
-    if drows != prob.rows:
-        raise ValueError("dy has %d rows, x has %d" % (drows, prob.rows))
-    dx = _new_rows(torch, x.shape, prob.x_stride, x) if need_dx else None
+    drows, _, ys = _rows(dy, "dy", f)
+    if drows != rows:
+        raise ValueError("dy has %d rows, x has %d" % (drows, rows))
+    dx = _new_rows(x.shape, xs, x) if need_dx else None
     dwg = torch.empty_like(wg) if need_dw else None
     dwu = torch.empty_like(wu) if need_dw else None
-    need = _gated_need(prob, OP_DGRAD, _off16(x, wg, wu))
-    ws, wp, wb = _ws(torch, ws, need, x.device)
-    with torch.cuda.device(x.device):
-        # an empty x has no dx to ask for
-        _check(lib().cnhwc_gated_bwd(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(dx), _ptr(dwg),
-                                     _ptr(dwu), wp, wb, _stream_handle(torch, x.device))
-               if prob.rows or need_dw else OK)
+    if rows or need_dw:          # an empty x has no dx to ask for
+        prob, need = _gated_desc(OP_DGRAD, _off16(x, wg, wu), rows, c, f, xs, ys, a, dt)
+        ws, wp, wb = _ws(ws, need, x.device)
+        _enqueue(lib().cnhwc_gated_bwd, x.device, prob, _ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(dx), _ptr(dwg),
+                 _ptr(dwu), wp, wb)
     return dx, dwg, dwu
 
 
@@ -530,8 +566,8 @@ def dropout(x, p, seed, offset=0, residual=None, y=None, device_offset=None):
     """residual + (keep ? x / (1 - p) : 0), the mask drawn by Philox4x32-10 from
     (seed, offset, element index).  device_offset: an int64 device tensor of one
     value that is added to offset when the kernel runs."""
-    import torch
-    _on_gpu(x, "x")
+    torch = _t()
+    dt = _operand(x, "x")
     rows, c, xs = _rows(x, "x")
     rs = 0
     if residual is not None:
@@ -543,14 +579,11 @@ def dropout(x, p, seed, offset=0, residual=None, y=None, device_offset=None):
         _same(device_offset, x, "device_offset", torch.int64)
         if device_offset.numel() != 1:
             raise ValueError("device_offset must hold one value")
-    for v, what in ((seed, "seed"), (offset, "offset")):
-        if not 0 <= v < 1 << 64:
-            raise ValueError("%s must be in [0, 2^64) (got %d)" % (what, v))
-    y, ys = _like_rows(y, x.shape, "y", rows, c, x)
-    prob = DropoutProblem(rows, c, xs, rs, ys, p, seed, offset, _mix_dtype(torch, x, "x"), 0)
-    with torch.cuda.device(x.device):
-        _check(lib().cnhwc_dropout(ctypes.byref(prob), _ptr(x), _ptr(residual), _ptr(y), _ptr(device_offset),
-                                   _stream_handle(torch, x.device)))
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must be in [0, 2^64) (got %d and %d)" % (seed, offset))
+    y, ys = _out(y, x.shape, "y", rows, c, x)
+    prob = DropoutProblem(rows, c, xs, rs, ys, p, seed, offset, dt, 0)
+    _enqueue(lib().cnhwc_dropout, x.device, ctypes.byref(prob), _ptr(x), _ptr(residual), _ptr(y), _ptr(device_offset))
     return y
 
 

@@ -53,9 +53,14 @@ constexpr int kGatedBig = 256, kGatedSmall = 128;
 int launch_gated_product(int dtype, GatedProduct prod, int tile, const GatedArgs& a, hipStream_t st);
 // Folds the partial sums of a split product into its result.
 int launch_gated_reduce(int dtype, GatedProduct prod, const GatedArgs& a, hipStream_t st);
-// dst [rows][ldd] = src [rows][cols] (row stride lds), columns cols..ldd-1 zero.
-int launch_gated_pack(const void* src, int64_t lds, int64_t rows, int64_t cols, void* dst, int64_t ldd,
-                      hipStream_t st);
+// Copies of up to three operands, one launch: dst [rows][ldd] = src [rows][cols]
+// (row stride ld), columns cols..ldd-1 zero.
+struct GatedPack {
+    const void* src;
+    void* dst;
+    int64_t ld, rows;
+};
+int launch_gated_pack(const GatedPack* p, int n, int64_t cols, int64_t ldd, hipStream_t st);
 // dst[0..n) = 0 (16-bit elements)
 int launch_gated_zero(void* dst, int64_t n, hipStream_t st);
 

@@ -768,10 +768,11 @@ template <typename T>
 __global__ __launch_bounds__(256) void gated_join_proj_kernel(const GatedArgs a) {
     const int64_t vecs = a.fp / 8, n = a.m * vecs;
     for (int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x; v < n; v += int64_t(gridDim.x) * 256) {
-        const int64_t m = v / vecs, f = (v - m * vecs) * 8;
+        const int64_t m = n <= 0xffffffffll ? int64_t(uint32_t(v) / uint32_t(vecs)) : v / vecs, f = (v - m * vecs) * 8;
         float g[8], u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.0f;
+#pragma unroll 4
         for (int s = 0; s < a.splits; ++s) {
             const float* p = a.part + (int64_t(s) * a.m + m) * a.part_ld + f;
 #pragma unroll
@@ -811,8 +812,9 @@ template <typename T, bool DW>
 __global__ __launch_bounds__(256) void gated_join_kernel(const GatedArgs a) {
     const int64_t vecs = a.part_ld / 4, n = a.m * vecs;
     for (int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x; v < n; v += int64_t(gridDim.x) * 256) {
-        const int64_t m = v / vecs, c = (v - m * vecs) * 4;
+        const int64_t m = n <= 0xffffffffll ? int64_t(uint32_t(v) / uint32_t(vecs)) : v / vecs, c = (v - m * vecs) * 4;
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
         for (int q = 0; q < a.splits; ++q)
             s += *reinterpret_cast<const f32x4*>(a.part + (int64_t(q) * a.m + m) * a.part_ld + c);
         char* row;
@@ -830,15 +832,21 @@ __global__ __launch_bounds__(256) void gated_join_kernel(const GatedArgs a) {
     }
 }
 
-// Rows copied to a wider, 16-byte-aligned stride with zeros behind them.
-__global__ __launch_bounds__(256) void gated_pack_kernel(const unsigned short* src, int64_t lds, int64_t rows,
-                                                         int64_t cols, unsigned short* dst, int64_t ldd) {
-    const int64_t vecs = ldd / 8, n = rows * vecs;
+// Rows copied to a wider, 16-byte-aligned stride with zeros behind them; one
+// operand per blockIdx.y.
+struct PackArgs {
+    GatedPack p[3];
+};
+__global__ __launch_bounds__(256) void gated_pack_kernel(const PackArgs a, int64_t cols, int64_t ldd) {
+    const GatedPack p = blockIdx.y == 0 ? a.p[0] : blockIdx.y == 1 ? a.p[1] : a.p[2];
+    const unsigned short* src = static_cast<const unsigned short*>(p.src);
+    unsigned short* dst = static_cast<unsigned short*>(p.dst);
+    const int64_t vecs = ldd / 8, n = p.rows * vecs;
     for (int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x; v < n; v += int64_t(gridDim.x) * 256) {
-        const int64_t r = v / vecs, c = (v - r * vecs) * 8;
+        const int64_t r = n <= 0xffffffffll ? int64_t(uint32_t(v) / uint32_t(vecs)) : v / vecs;
+        const int64_t c = (v - r * vecs) * 8;
         const int left = int(cols - c < 8 ? cols - c : 8);
-        const i32x4 x = load_n<F16>(reinterpret_cast<const char*>(src + r * lds + c), left);
-        *reinterpret_cast<i32x4*>(dst + r * ldd + c) = x;
+        *reinterpret_cast<i32x4*>(dst + r * ldd + c) = load_n<F16>(reinterpret_cast<const char*>(src + r * p.ld + c), left);
     }
 }
 
@@ -908,10 +916,14 @@ int launch_gated_reduce(int dtype, GatedProduct prod, const GatedArgs& a, hipStr
     return CNHWC_OK;
 }
 
-int launch_gated_pack(const void* src, int64_t lds, int64_t rows, int64_t cols, void* dst, int64_t ldd,
-                      hipStream_t st) {
-    gated_pack_kernel<<<blocks_for(rows * (ldd / 8)), 256, 0, st>>>(static_cast<const unsigned short*>(src), lds, rows,
-                                                                    cols, static_cast<unsigned short*>(dst), ldd);
+int launch_gated_pack(const GatedPack* p, int n, int64_t cols, int64_t ldd, hipStream_t st) {
+    PackArgs a = {};
+    int64_t most = 0;
+    for (int i = 0; i < n; ++i) {
+        a.p[i] = p[i];
+        most = p[i].rows > most ? p[i].rows : most;
+    }
+    gated_pack_kernel<<<dim3(blocks_for(most * (ldd / 8)), n), 256, 0, st>>>(a, cols, ldd);
     return CNHWC_OK;
 }
 

@@ -173,31 +173,36 @@ struct Shape {
     int64_t tiles_m, tiles_n;
 };
 
-// Estimated time of each choice in steps of the big tile, the least one wins.
-// One CU runs one big block or two small ones; a round of small blocks does
-// half a big round's work per step in more than half its time, so small tiles
-// win where big ones leave CUs idle.
-Shape choose_shape(int64_t m, int64_t n, int64_t steps, bool dual) {
+// Estimated microseconds of each choice, the least one wins.  The rates are
+// measured (bf16 normal operands, one product at a time): a 64-deep step of the
+// 256 x 256 tile takes 1.55 us (1.65 where an operand is read transposed), of
+// two 128 x 128 tiles sharing a CU 0.95 us (1.0), of one alone 0.7 us; a tile's
+// start and results cost `fixed` on top (the backward projections read dy and
+// write twice the forward's); partial sums move at 8 TB/s, mostly within the
+// caches, and the joining launch costs 3.5 us.  So small tiles win where large
+// ones leave CUs idle or the reduction is short, and a reduction is split into
+// as many parts as fill the CUs.  For example 50176 x 384 -> 1024: dx on small
+// tiles 93 us, on large ones 112 us; dwg and dwu in 16 splits of the large tile
+// 99 us, unsplit on small tiles 617 us.
+Shape choose_shape(GatedProduct prod, int end, int64_t m, int64_t n, int64_t steps) {
     const cnhwc_override& ov = current_override();
+    const bool dual = prod == kProj;
     Shape best = {0, 0, 0, 0};
     double best_cost = 0;
     for (int tile : {kGatedBig, kGatedSmall}) {
         if ((ov.tune == kGatedBig || ov.tune == kGatedSmall) && ov.tune != tile) continue;
+        const bool big = tile == kGatedBig;
         const int64_t tm = ceil_div(m, tile), tn = ceil_div(n, dual ? tile / 2 : tile);
-        const int64_t slots = tile == kGatedBig ? kNumCUs : 2 * kNumCUs;
-        const double step_cost = tile == kGatedBig ? 1.0 : 0.6;
-        const double fixed = tile == kGatedBig ? 6.0 : 4.0;   // prologue, results
-        // one split per power of two, each at least four steps deep
-        const int64_t forced = std::min<int64_t>(ov.split_c, steps);
-        for (int64_t s = forced > 0 ? forced : 1; s <= 64 && (s == 1 || s == forced || steps / s >= 4);
-             s = forced > 0 ? 65 : s * 2) {
-            const int64_t rounds = ceil_div(tm * tn * s, slots);
-            double cost = double(rounds) * (double(ceil_div(steps, s)) * step_cost + fixed);
-            if (s > 1) {
-                // partial sums written and read at a few TB/s, and one more launch
-                const double bytes = double(tm * tn * s) * tile * tile * 8;
-                cost += 4.0 + bytes / 4.0e6;
-            }
+        const double step = big ? (dual ? 1.55 : 1.65) : (dual ? 0.95 : 1.0), step_alone = big ? step : 0.7;
+        const double fixed = dual ? (end == kEndBwd ? (big ? 10.0 : 4.5) : (big ? 4.5 : 2.5)) : (big ? 5.0 : 3.5);
+        const int64_t slots = big ? kNumCUs : 2 * kNumCUs;
+        const int64_t forced = std::min<int64_t>(std::min(ov.split_c, 64), steps);
+        const int64_t lo = forced > 0 ? forced : 1, hi = forced > 0 ? forced : 64;
+        for (int64_t s = lo; s <= hi && (s == lo || steps / s >= 4); ++s) {
+            const int64_t tiles = tm * tn * s, deep = ceil_div(steps, s), rest = tiles % slots;
+            double cost = double(tiles / slots) * (double(deep) * step + fixed);
+            if (rest) cost += double(deep) * (rest <= kNumCUs ? step_alone : step) + fixed;
+            if (s > 1) cost += 3.5 + double(m) * double(dual ? 2 * n : n) * double(s) * 8 / 8.0e6;
             if (best.tile == 0 || cost < best_cost) {
                 best = {tile, int(s), tm, tn};
                 best_cost = cost;
@@ -242,12 +247,12 @@ GatedPlan plan_gated(const Gated& p, int op, bool x_off, bool w_off) {
         g.off_wu = take(p.f * g.cp * 2);
     }
     const int64_t csteps = ceil_div(g.cp, 64);
-    g.proj = choose_shape(p.rows, p.f, csteps, true);
+    g.proj = choose_shape(kProj, op == CNHWC_OP_FWD ? kEndFwd : kEndBwd, p.rows, p.f, csteps);
     int64_t part = part_bytes(g.proj, p.rows, 2 * g.fp);
     if (op != CNHWC_OP_FWD) {
         g.off_dgu = take(p.rows * 2 * g.fp * 2);
-        g.dx = choose_shape(p.rows, p.c, 2 * ceil_div(g.fp, 64), false);
-        g.dw = choose_shape(2 * g.fp, p.c, ceil_div(p.rows, 64), false);
+        g.dx = choose_shape(kDx, kEndFwd, p.rows, p.c, 2 * ceil_div(g.fp, 64));
+        g.dw = choose_shape(kDw, kEndFwd, 2 * g.fp, p.c, ceil_div(p.rows, 64));
         part = std::max(part, std::max(part_bytes(g.dx, p.rows, up(p.c, 4)), part_bytes(g.dw, 2 * g.fp, up(p.c, 4))));
     }
     if (part) g.off_part = take(part);
@@ -338,19 +343,22 @@ int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const voi
     char* w = static_cast<char*>(ws);
     const void *xo = x, *go = wg, *uo = wu;
     int64_t ldx = p.xs;
+    GatedPack pack[3];
+    int packs = 0;
     if (g.pack_x) {
-        launch_gated_pack(x, p.xs, p.rows, p.c, w + g.off_x, g.cp, st);
-        if ((rc = launched("gated_pack"))) return rc;
+        pack[packs++] = {x, w + g.off_x, p.xs, p.rows};
         xo = w + g.off_x;
         ldx = g.cp;
     }
     if (g.pack_w) {
-        launch_gated_pack(wg, p.c, p.f, p.c, w + g.off_wg, g.cp, st);
-        if ((rc = launched("gated_pack"))) return rc;
-        launch_gated_pack(wu, p.c, p.f, p.c, w + g.off_wu, g.cp, st);
-        if ((rc = launched("gated_pack"))) return rc;
+        pack[packs++] = {wg, w + g.off_wg, p.c, p.f};
+        pack[packs++] = {wu, w + g.off_wu, p.c, p.f};
         go = w + g.off_wg;
         uo = w + g.off_wu;
+    }
+    if (packs) {
+        launch_gated_pack(pack, packs, p.c, g.cp, st);
+        if ((rc = launched("gated_pack"))) return rc;
     }
     GatedArgs a;
     std::memset(&a, 0, sizeof a);

@@ -110,7 +110,7 @@ def test_layernorm_parts():
     dy = rnd(5, 2, 5, 6, 48).to(t).cuda()
     full = api.layernorm_bwd(dy, x, mean, rstd, gamma)
     import ctypes
-    q = api._ln_problem(torch, x, gamma, None, 0.0, 48, 60, 48, 48)
+    q = api.LayernormProblem(60, 48, 48, 48, 0.0, api.BF16, api.BF16, 0)
     st = torch.cuda.current_stream().cuda_stream
     ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
     for i in range(3):

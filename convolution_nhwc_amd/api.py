@@ -342,7 +342,7 @@ def _operand(t, what, f32=True):
 def _out(t, shape, what, rows, width, ref):
     """(output, its row stride): the caller's, or a new dense one."""
     if t is None:
-        return _torch.empty(shape, dtype=ref.dtype, device=ref.device), width
+        return ref.new_empty(shape), width
     _same(t, ref, what)
     r, _, st = _rows(t, what, width)
     if r != rows:
@@ -430,8 +430,8 @@ def layernorm(x, gamma=None, beta=None, eps=1e-5, y=None):
     y, ys = _out(y, x.shape, "y", rows, c, x)
     prob, _ = _ln_desc(rows, c, xs, ys, eps, dt, pd)
     dev = x.device
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
     _enqueue(lib().cnhwc_layernorm_fwd, dev, prob, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
@@ -470,8 +470,8 @@ def layernorm_bwd(dy, x, mean, rstd, gamma=None, dx=None, param_dtype=None, ws=N
         if _rows(dx, "dx", c)[::2] != (rows, xs):
             raise ValueError("dx must have x's rows and row stride (%d)" % xs)
     dev = x.device
-    dgamma = torch.empty(c, dtype=ptype, device=dev)
-    dbeta = torch.empty(c, dtype=ptype, device=dev)
+    dgamma = x.new_empty((c,), dtype=ptype)
+    dbeta = x.new_empty((c,), dtype=ptype)
     prob, need = _ln_desc(rows, c, xs, ys, 0.0, dt, pd)
     ws, wp, wb = _ws(ws, need, dev)
     _enqueue(lib().cnhwc_layernorm_bwd, dev, prob, _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
@@ -484,8 +484,8 @@ def _new_rows(shape, stride, ref):
     dx the row stride of x)."""
     c = shape[-1]
     if stride == c:
-        return _torch.empty(shape, dtype=ref.dtype, device=ref.device)
-    return _torch.empty((*shape[:-1], stride), dtype=ref.dtype, device=ref.device)[..., :c]
+        return ref.new_empty(shape)
+    return ref.new_empty((*shape[:-1], stride))[..., :c]
 
 
 def _gated_operands(x, wg, wu, act):

@@ -1,106 +1,177 @@
 // Gated feed-forward for few rows (decoding, small serving batches): every
 // weight is read once, so the call is bound by streaming wg and wu.
 //
-// A block owns 16 hidden units.  Its waves split the reduction in chunks of 64
-// channels; a lane reads 32 contiguous bytes of one weight row per chunk (a
-// quarter of a 128-byte line, the wave reads whole lines) straight into the
-// matrix instruction's operand registers: the two 32-deep products of a chunk
-// take the lane's first and second 8 channels, an order of the reduction that
-// x follows.  x comes from the L2.  The waves' sums are added through LDS in
-// wave order.
+// A weight tile is the 16 rows of a matrix instruction: 8 hidden units' rows
+// of wg and the same of wu, so that one instruction gives g and u of 8 units
+// for 16 rows of x.  The waves of a block split the reduction in chunks of 64
+// channels; a lane reads 16 contiguous bytes of one row per 32-deep product
+// straight into the instruction's operand registers.  The waves' sums are
+// added through LDS in wave order.
+//
+// gated_rows_kernel is one persistent block of 16 (or 8) waves a CU: a wave's share
+// of x stays in its registers for all of the block's tiles, and the next
+// tile's weights are on their way while the current one is added up.  With
+// blocks of one tile instead, every tile read x again through the L2, which at
+// 24 rows cost as much as the weights (2048 -> 5504 fp16: 16.8 us, of which 12.9
+// without x).  Where a wave's share of x does not fit (gated_rows_wide_kernel:
+// long rows, many of them) x is read per tile.
 #include "gated.h"
 
 namespace cnhwc {
 namespace {
 
-template <typename T, int MT, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void gated_rows_kernel(const GatedRowsArgs a) {
-    __shared__ float sums[WAVES][2][MT][16][17];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int fr = lane & 15, grp = lane >> 4;
-    const int64_t f0 = int64_t(blockIdx.x) * 16;
-    // rows past the end read the last one: their results are not stored
-    const int64_t fw = f0 + fr < a.f ? f0 + fr : a.f - 1;
-    const char* gp = static_cast<const char*>(a.wg) + (fw * a.c + grp * 16) * 2;
-    const char* up = static_cast<const char*>(a.wu) + (fw * a.c + grp * 16) * 2;
-    const char* xp[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int64_t r = t * 16 + fr;
-        xp[t] = static_cast<const char*>(a.x) + ((r < a.rows ? r : a.rows - 1) * a.ldx + grp * 16) * 2;
+// This lane's source in the weights: unit fr % 8 of the tile, wg for the first
+// 8 lanes and wu for the others.  Units past the end read the last one: their
+// results are not stored.
+__device__ __attribute__((always_inline)) inline const char* weight_row(const GatedRowsArgs& a, int64_t tile, int fr) {
+    const int64_t f = tile * 8 + (fr & 7);
+    return static_cast<const char*>(fr < 8 ? a.wg : a.wu) + (f < a.f ? f : a.f - 1) * a.c * 2;
+}
+__device__ __attribute__((always_inline)) inline const char* x_row(const GatedRowsArgs& a, int64_t r) {
+    return static_cast<const char*>(a.x) + (r < a.rows ? r : a.rows - 1) * a.ldx * 2;
+}
+
+// The two 32-deep operands of the chunk of 64 channels from k on; channels
+// past c read as 0.
+template <typename T>
+__device__ __attribute__((always_inline)) inline void load_chunk(i32x4 (&r)[2], const char* row, int64_t k, int64_t c,
+                                                                 int grp) {
+    const char* p = row + (k + grp * 8) * 2;
+    if (k + 64 <= c) {
+        r[0] = load16<T>(p);
+        r[1] = load16<T>(p + 64);
+    } else {
+        const int64_t left = c - k - grp * 8;
+        r[0] = load_n<T>(p, int(left));
+        r[1] = load_n<T>(p + 64, int(left - 32));
     }
-    f32x4 ag[MT], au[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) ag[t] = au[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
 
-    auto chunk = [&](int64_t k, auto whole) {
-        constexpr bool W = decltype(whole)::value != 0;
-        i32x4 g[2], u[2], x[MT][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t o = (k + h * 8) * 2;
-            const int left = W ? 8 : int(a.c - (k + grp * 16 + h * 8));
-            if constexpr (W) {
-                g[h] = load16<T>(gp + o);
-                u[h] = load16<T>(up + o);
-            } else {
-                g[h] = load_n<T>(gp + o, left);
-                u[h] = load_n<T>(up + o, left);
-            }
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                if constexpr (W) x[t][h] = load16<T>(xp[t] + o);
-                else x[t][h] = load_n<T>(xp[t] + o, left);
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                ag[t] = mfma16x16x32<T>(g[h], x[t][h], ag[t]);
-                au[t] = mfma16x16x32<T>(u[h], x[t][h], au[t]);
-            }
-    };
-    const int64_t whole = a.c / 64;
-    int64_t q = wave;
-#pragma unroll 4
-    for (; q < whole; q += WAVES) chunk(q * 64, IC<1>{});
-    if (q == whole && a.c % 64) chunk(q * 64, IC<0>{});
-
-    // lane: hidden units 4*grp..+3 of row t*16 + fr
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            sums[wave][0][t][fr][4 * grp + e] = ag[t][e];
-            sums[wave][1][t][fr][4 * grp + e] = au[t][e];
-        }
-    __syncthreads();
-    for (int i = tid; i < MT * 256; i += WAVES * 64) {
-        const int t = i >> 8, r = (i >> 4) & 15, c = i & 15;
-        const int64_t row = t * 16 + r, f = f0 + c;
+// Adds the waves' sums of one tile and stores its results.
+template <typename T, int MT, int WAVES>
+__device__ __attribute__((always_inline)) inline void finish_tile(const GatedRowsArgs& a, const float (*sums)[MT][16][17],
+                                                                  int64_t tile) {
+    for (int i = threadIdx.x; i < MT * 128; i += WAVES * 64) {
+        const int c = i & 7, r = (i >> 3) & 15, t = i >> 7;
+        const int64_t row = t * 16 + r, f = tile * 8 + c;
         if (row < a.rows && f < a.f) {
             float g = 0.0f, u = 0.0f;
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) {
-                g += sums[w][0][t][r][c];
-                u += sums[w][1][t][r][c];
+                g += sums[w][t][r][c];
+                u += sums[w][t][r][c + 8];
             }
             store1<T>(static_cast<char*>(a.y) + (row * a.ldy + f) * 2, act_value(a.act, g) * u);
         }
     }
 }
 
+// MT: 16-row tiles of x; NC: chunks a wave.
+template <typename T, int MT, int WAVES, int NC>
+__global__ __launch_bounds__(WAVES * 64) void gated_rows_kernel(const GatedRowsArgs a) {
+    __shared__ float sums[2][WAVES][MT][16][17];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, grp = lane >> 4;
+    const int64_t tiles = (a.f + 7) / 8;
+    i32x4 w[NC][2], next[NC][2], x[NC][MT][2];
+    auto fetch = [&](int64_t tile) __attribute__((always_inline)) {
+        const char* row = weight_row(a, tile < tiles ? tile : tiles - 1, fr);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) load_chunk<T>(next[i], row, int64_t(wave + i * WAVES) * 64, a.c, grp);
+    };
+    fetch(blockIdx.x);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            load_chunk<T>(x[i][t], x_row(a, t * 16 + fr), int64_t(wave + i * WAVES) * 64, a.c, grp);
+    int buf = 0;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) w[i][h] = next[i][h];
+        if (tile + gridDim.x < tiles) fetch(tile + gridDim.x);
+        __builtin_amdgcn_sched_barrier(0);   // the next tile's loads go out before this one's are waited for
+        f32x4 acc[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[t] = mfma16x16x32<T>(w[i][h], x[i][t][h], acc[t]);
+        // lane: units 4*grp..+3 of (g | u), row t*16 + fr
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sums[buf][wave][t][fr][4 * grp + e] = acc[t][e];
+        // one barrier a tile: a wave writes this buffer again only after the
+        // next tile's barrier, which it shares with those still reading here
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+        finish_tile<T, MT, WAVES>(a, sums[buf], tile);
+        buf ^= 1;
+    }
+}
+
+// One tile a block, x read with the weights, D chunks at a time.
+template <typename T, int MT, int WAVES, int D>
+__global__ __launch_bounds__(WAVES * 64) void gated_rows_wide_kernel(const GatedRowsArgs a) {
+    __shared__ float sums[WAVES][MT][16][17];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, grp = lane >> 4;
+    const char* row = weight_row(a, blockIdx.x, fr);
+    const char* xp[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xp[t] = x_row(a, t * 16 + fr);
+    f32x4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t chunks = (a.c + 63) / 64;
+    for (int64_t q = wave; q < chunks; q += D * WAVES) {
+        i32x4 w[D][2], x[D][MT][2];
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            load_chunk<T>(w[d], row, (q + d * WAVES) * 64, a.c, grp);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) load_chunk<T>(x[d][t], xp[t], (q + d * WAVES) * 64, a.c, grp);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // every load is issued before the first product waits
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[t] = mfma16x16x32<T>(w[d][h], x[d][t][h], acc[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[wave][t][fr][4 * grp + e] = acc[t][e];
+    __syncthreads();
+    finish_tile<T, MT, WAVES>(a, sums, blockIdx.x);
+}
+
+template <typename T, int MT, int WAVES, int NC>
+void launch_kept(const GatedRowsArgs& a, hipStream_t st) {
+    const int64_t tiles = (a.f + 7) / 8;
+    const dim3 grid((unsigned)(tiles < kNumCUs ? tiles : kNumCUs));
+    gated_rows_kernel<T, MT, WAVES, NC><<<grid, WAVES * 64, 0, st>>>(a);
+}
+
 template <typename T, int MT>
 void launch(const GatedRowsArgs& a, hipStream_t st) {
-    const int64_t blocks = (a.f + 15) / 16;
-    // enough waves to keep the memory busy: 8 a CU where the reduction has
-    // that many chunks
-    const int64_t chunks = (a.c + 63) / 64;
-    if (MT <= 2 && blocks * 4 < kNumCUs * 8 && chunks >= 16)
-        gated_rows_kernel<T, MT, MT <= 2 ? 8 : 4><<<dim3((unsigned)blocks), MT <= 2 ? 512 : 256, 0, st>>>(a);
-    else
-        gated_rows_kernel<T, MT, 4><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+    // a wave has 128 registers in a block of 16 and 256 in one of 8; its chunks
+    // of x take 8 * MT of them each, two tiles' weights 16
+    constexpr int W = MT == 4 ? 8 : 16, MOST = MT == 2 ? 2 : 4;
+    const int64_t nc = ((a.c + 63) / 64 + W - 1) / W;
+    if (nc == 1) launch_kept<T, MT, W, 1>(a, st);
+    else if (nc == 2) launch_kept<T, MT, W, 2>(a, st);
+    else if (nc <= MOST) launch_kept<T, MT, W, MOST>(a, st);
+    else gated_rows_wide_kernel<T, MT, 8, MT == 1 ? 4 : MT == 2 ? 2 : 1><<<dim3((unsigned)((a.f + 7) / 8)), 512, 0, st>>>(a);
 }
 
 template <typename T>

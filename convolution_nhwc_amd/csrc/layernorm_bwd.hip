@@ -17,7 +17,7 @@ __global__ __launch_bounds__(L > 256 ? L : 256) void ln_bwd_kernel(const LnArgs 
     constexpr int V = kVec<T>, ES = kElemBytes<T>, PS = kElemBytes<P>;
     constexpr int THREADS = L > 256 ? L : 256, RPB = THREADS / L, WAVES = THREADS / 64;
     constexpr bool JOIN = COLS && L <= 64;       // several waves hold the same columns
-    __shared__ float red[2][16];
+    __shared__ float2 red[2][16];
     __shared__ float join[JOIN ? WAVES * L * NV * V : 1];
     int phase = 0;
     const int li = threadIdx.x % L;
@@ -28,49 +28,74 @@ __global__ __launch_bounds__(L > 256 ? L : 256) void ln_bwd_kernel(const LnArgs 
 #pragma unroll
             for (int e = 0; e < V; ++e) dg[i][e] = db[i][e] = 0.0f;
     }
-    for (int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / L; row < a.rows; row += int64_t(gridDim.x) * RPB) {
-        const char* xp = static_cast<const char*>(a.x) + row * a.x_stride * ES;
-        const char* dp = static_cast<const char*>(a.dy) + row * a.y_stride * ES;
-        i32x4 x[NV], dy[NV];
+    float gamma[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) gamma[i][e] = 1.0f;
+    if (a.gamma) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c0 = (i * L + li) * V;
-            x[i] = load_n<T>(xp + int64_t(c0) * ES, a.c - c0);
-            dy[i] = load_n<T>(dp + int64_t(c0) * ES, a.c - c0);
+#pragma unroll
+            for (int h = 0; h < V; h += kVec<P>) {
+                const i32x4 w = load_n<P>(static_cast<const char*>(a.gamma) + int64_t(c0 + h) * PS, a.c - c0 - h);
+#pragma unroll
+                for (int e = 0; e < kVec<P> && e < V; ++e) gamma[i][h + e] = elem<P>(w, e);
+            }
         }
-        const float mean = a.mean[row], rstd = a.rstd[row];
+    }
+    // a row's loads are issued before the row ahead of it is summed (but for
+    // the widest rows, whose 1024 threads have 128 registers each)
+    constexpr bool AHEAD = L < 1024;
+    i32x4 nx[NV], ndy[NV];
+    float nmean = 0.0f, nrstd = 0.0f;
+    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+        const bool any = row < a.rows;
+        const char* xp = static_cast<const char*>(a.x) + row * a.x_stride * ES;
+        const char* dp = static_cast<const char*>(a.dy) + row * a.y_stride * ES;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c0 = (i * L + li) * V;
+            nx[i] = load_n<T>(xp + int64_t(c0) * ES, any ? a.c - c0 : 0);
+            ndy[i] = load_n<T>(dp + int64_t(c0) * ES, any ? a.c - c0 : 0);
+        }
+        if (any) {
+            nmean = a.mean[row];
+            nrstd = a.rstd[row];
+        }
+    };
+    const int64_t first = int64_t(blockIdx.x) * RPB + threadIdx.x / L, stride = int64_t(gridDim.x) * RPB;
+    if (AHEAD) fetch(first);
+    for (int64_t row = first; row < a.rows; row += stride) {
+        if (!AHEAD) fetch(row);
+        i32x4 x[NV], dy[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = nx[i];
+            dy[i] = ndy[i];
+        }
+        const float mean = nmean, rstd = nrstd;
+        if (AHEAD) fetch(row + stride);
         float s1 = 0.0f, s2 = 0.0f;
         float g[NV][V];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c0 = (i * L + li) * V, left = a.c - c0;
-#pragma unroll
-            for (int e = 0; e < V; ++e) g[i][e] = elem<T>(dy[i], e);
-            if (a.gamma) {
-#pragma unroll
-                for (int h = 0; h < V; h += kVec<P>) {
-                    const i32x4 w = load_n<P>(static_cast<const char*>(a.gamma) + int64_t(c0 + h) * PS, left - h);
-#pragma unroll
-                    for (int e = 0; e < kVec<P> && e < V; ++e) g[i][h + e] *= elem<P>(w, e);
-                }
-            }
+            // (columns past c hold dy = 0, which adds nothing to any sum)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float xh = (elem<T>(x[i], e) - mean) * rstd;
-                // columns past c hold dy = 0 and x = 0: xhat there is not used
-                if (e < left) {
-                    s1 += g[i][e];
-                    s2 += g[i][e] * xh;
-                    if constexpr (COLS) {
-                        const float d = elem<T>(dy[i], e);
-                        dg[i][e] += d * xh;
-                        db[i][e] += d;
-                    }
+                const float d = elem<T>(dy[i], e), xh = (elem<T>(x[i], e) - mean) * rstd;
+                g[i][e] = d * gamma[i][e];
+                s1 += g[i][e];
+                s2 += g[i][e] * xh;
+                if constexpr (COLS) {
+                    dg[i][e] += d * xh;
+                    db[i][e] += d;
                 }
             }
         }
-        const float m1 = row_sum<L>(s1, red, phase) / a.cf;
-        const float m2 = row_sum<L>(s2, red, phase) / a.cf;
+        row_sum2<L>(s1, s2, red, phase);
+        const float m1 = s1 / a.cf, m2 = s2 / a.cf;
         if (a.y) {
             char* op = static_cast<char*>(a.y) + row * a.x_stride * ES;
 #pragma unroll
@@ -255,7 +280,7 @@ void launch_lanes(const LnArgs& a, int nv, int blocks, hipStream_t st) {
 
 template <typename T, typename P>
 void launch(int dtype, const LnArgs& a, int blocks, hipStream_t st) {
-    const LnShape s = ln_shape(a.c, dtype, kBwdMaxVecs);
+    const LnShape s = ln_shape(a.rows, a.c, dtype, kBwdMaxVecs);
     switch (s.lanes) {
     case 16: launch_lanes<T, P, 16>(a, s.nv, blocks, st); break;
     case 64: launch_lanes<T, P, 64>(a, s.nv, blocks, st); break;
@@ -277,17 +302,17 @@ void launch(int dtype, const LnArgs& a, int blocks, hipStream_t st) {
 
 int layernorm_bwd_blocks(int dtype, int64_t rows, int64_t c) {
     if (rows <= 0) return 0;
-    const LnShape s = ln_shape(c, dtype, kBwdMaxVecs);
+    const LnShape s = ln_shape(rows, c, dtype, kBwdMaxVecs);
     if (s.lanes == 0) return int(rows < 64 ? rows : 64);
     const int rpb = s.lanes > 256 ? 1 : 256 / s.lanes;
     const int64_t steps = (rows + rpb - 1) / rpb;
     // a block's partial sums cost 16 bytes of traffic a column (written and
-    // read), a row in 16 bits 6: eight row steps a block keep them small,
-    // as long as every CU has a block
-    const int64_t cap = int64_t(kNumCUs) * (s.lanes > 256 ? 1 : 4);
+    // read), a row in 16 bits 6: at least eight row steps a block, once every
+    // CU has four blocks (two where a row takes a whole one of 1024 threads)
+    const int64_t full = int64_t(kNumCUs) * (s.lanes > 256 ? 2 : 4);
     int64_t b = (steps + 7) / 8;
     if (b < kNumCUs) b = steps < kNumCUs ? steps : kNumCUs;
-    return int(b < cap ? b : cap);
+    return int(b < full ? b : full);
 }
 
 int launch_layernorm_bwd(int dtype, int param_dtype, const LnArgs& a, int blocks, hipStream_t st) {

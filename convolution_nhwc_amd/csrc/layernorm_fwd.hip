@@ -33,10 +33,18 @@ __global__ __launch_bounds__(L > 256 ? L : 256) void ln_fwd_kernel(const LnArgs 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int left = a.c - (i * L + li) * V;
+            if (left >= V) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = elem<T>(x[i], e) - mean;
-                if (e < left) q += d * d;
+                for (int e = 0; e < V; ++e) {
+                    const float d = elem<T>(x[i], e) - mean;
+                    q += d * d;
+                }
+            } else if (left > 0) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float d = elem<T>(x[i], e) - mean;
+                    if (e < left) q += d * d;
+                }
             }
         }
         const float rstd = 1.0f / sqrtf(row_sum<L>(q, red, phase) / a.cf + a.eps);
@@ -140,7 +148,7 @@ void launch_lanes(const LnArgs& a, int nv, hipStream_t st) {
 
 template <typename T, typename P>
 void launch(int dtype, const LnArgs& a, hipStream_t st) {
-    const LnShape s = ln_shape(a.c, dtype, 4096);
+    const LnShape s = ln_shape(a.rows, a.c, dtype, 4096);
     switch (s.lanes) {
     case 16: launch_lanes<T, P, 16>(a, s.nv, st); break;
     case 64: launch_lanes<T, P, 64>(a, s.nv, st); break;

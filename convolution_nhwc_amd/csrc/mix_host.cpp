@@ -178,8 +178,8 @@ struct Shape {
 // 256 x 256 tile takes 1.55 us (1.65 where an operand is read transposed), of
 // two 128 x 128 tiles sharing a CU 0.95 us (1.0), of one alone 0.7 us; a tile's
 // start and results cost `fixed` on top (the backward projections read dy and
-// write twice the forward's); partial sums move at 8 TB/s, mostly within the
-// caches, and the joining launch costs 3.5 us.  So small tiles win where large
+// write twice the forward's); partial sums move at 6 TB/s, mostly within the
+// caches, and the joining launch costs 5 us.  So small tiles win where large
 // ones leave CUs idle or the reduction is short, and a reduction is split into
 // as many parts as fill the CUs.  For example 50176 x 384 -> 1024: dx on small
 // tiles 93 us, on large ones 112 us; dwg and dwu in 16 splits of the large tile
@@ -202,7 +202,7 @@ Shape choose_shape(GatedProduct prod, int end, int64_t m, int64_t n, int64_t ste
             const int64_t tiles = tm * tn * s, deep = ceil_div(steps, s), rest = tiles % slots;
             double cost = double(tiles / slots) * (double(deep) * step + fixed);
             if (rest) cost += double(deep) * (rest <= kNumCUs ? step_alone : step) + fixed;
-            if (s > 1) cost += 3.5 + double(m) * double(dual ? 2 * n : n) * double(s) * 8 / 8.0e6;
+            if (s > 1) cost += 5.0 + double(m) * double(dual ? 2 * n : n) * double(s) * 8 / 6.0e6;
             if (best.tile == 0 || cost < best_cost) {
                 best = {tile, int(s), tm, tn};
                 best_cost = cost;

@@ -106,7 +106,7 @@ __device__ inline float act_value(int act, float g) {
         float e;
         return g * normal_cdf(g, e);
     }
-    case CNHWC_ACT_RELU: return g > 0.0f ? g : (g != g ? g : 0.0f);
+    case CNHWC_ACT_RELU: return g < 0.0f ? 0.0f : g;   // (NaN stays)
     default: return sigmoid_f(g);
     }
 }
@@ -128,7 +128,7 @@ __device__ inline void act_both(int act, float g, float& v, float& d) {
         break;
     }
     case CNHWC_ACT_RELU:
-        v = g > 0.0f ? g : (g != g ? g : 0.0f);
+        v = g < 0.0f ? 0.0f : g;
         d = g > 0.0f ? 1.0f : 0.0f;
         break;
     default: {

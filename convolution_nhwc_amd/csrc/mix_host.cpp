@@ -167,15 +167,18 @@ int validate(const cnhwc_gated_problem* q, Gated* o) {
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The tile and the number of reduction splits of one product.
+// The tile and the number of reduction splits of one product.  head > 0: the
+// first `head` rows run on the large tile in whole rounds of the GPU, the others
+// in a second launch on the small one.
 struct Shape {
     int tile, splits;
     int64_t tiles_m, tiles_n;
+    int64_t head;
 };
 
 // Estimated microseconds of each choice, the least one wins.  The rates are
 // measured (bf16 normal operands, one product at a time): a 64-deep step of the
-// 256 x 256 tile takes 1.55 us (1.65 where an operand is read transposed), of
+// 256 x 256 tile takes 1.45 us (1.55 where an operand is read transposed), of
 // two 128 x 128 tiles sharing a CU 0.95 us (1.0), of one alone 0.7 us; a tile's
 // start and results cost `fixed` on top (the backward projections read dy and
 // write twice the forward's); partial sums move at 6 TB/s, mostly within the
@@ -187,27 +190,40 @@ struct Shape {
 Shape choose_shape(GatedProduct prod, int end, int64_t m, int64_t n, int64_t steps) {
     const cnhwc_override& ov = current_override();
     const bool dual = prod == kProj;
-    Shape best = {0, 0, 0, 0};
-    double best_cost = 0;
-    for (int tile : {kGatedBig, kGatedSmall}) {
-        if ((ov.tune == kGatedBig || ov.tune == kGatedSmall) && ov.tune != tile) continue;
+    // unsplit, or `s` splits of it
+    auto cost_of = [&](int tile, int64_t rows, int64_t s) -> double {
         const bool big = tile == kGatedBig;
-        const int64_t tm = ceil_div(m, tile), tn = ceil_div(n, dual ? tile / 2 : tile);
-        const double step = big ? (dual ? 1.55 : 1.65) : (dual ? 0.95 : 1.0), step_alone = big ? step : 0.7;
-        const double fixed = dual ? (end == kEndBwd ? (big ? 10.0 : 4.5) : (big ? 4.5 : 2.5)) : (big ? 5.0 : 3.5);
+        const int64_t tm = ceil_div(rows, tile), tn = ceil_div(n, dual ? tile / 2 : tile);
+        const double step = big ? (dual ? 1.45 : 1.55) : (dual ? 0.95 : 1.0), step_alone = big ? step : 0.7;
+        const double fixed = dual ? (end == kEndBwd ? (big ? 8.0 : 4.5) : (big ? 4.0 : 2.5)) : (big ? 5.0 : 3.5);
         const int64_t slots = big ? kNumCUs : 2 * kNumCUs;
+        const int64_t tiles = tm * tn * s, deep = ceil_div(steps, s), rest = tiles % slots;
+        double cost = double(tiles / slots) * (double(deep) * step + fixed);
+        if (rest) cost += double(deep) * (rest <= kNumCUs ? step_alone : step) + fixed;
+        if (s > 1) cost += 5.0 + double(rows) * double(dual ? 2 * n : n) * double(s) * 8 / 6.0e6;
+        return cost;
+    };
+    Shape best = {0, 0, 0, 0, 0};
+    double best_cost = 0;
+    auto offer = [&](int tile, int64_t s, int64_t head, double cost) {
+        if (best.tile != 0 && cost >= best_cost) return;
+        best = {tile, int(s), ceil_div(m, tile), ceil_div(n, dual ? tile / 2 : tile), head};
+        best_cost = cost;
+    };
+    const bool forced_tile = ov.tune == kGatedBig || ov.tune == kGatedSmall;
+    for (int tile : {kGatedBig, kGatedSmall}) {
+        if (forced_tile && ov.tune != tile) continue;
         const int64_t forced = std::min<int64_t>(std::min(ov.split_c, 64), steps);
         const int64_t lo = forced > 0 ? forced : 1, hi = forced > 0 ? forced : 64;
-        for (int64_t s = lo; s <= hi && (s == lo || steps / s >= 4); ++s) {
-            const int64_t tiles = tm * tn * s, deep = ceil_div(steps, s), rest = tiles % slots;
-            double cost = double(tiles / slots) * (double(deep) * step + fixed);
-            if (rest) cost += double(deep) * (rest <= kNumCUs ? step_alone : step) + fixed;
-            if (s > 1) cost += 5.0 + double(m) * double(dual ? 2 * n : n) * double(s) * 8 / 6.0e6;
-            if (best.tile == 0 || cost < best_cost) {
-                best = {tile, int(s), tm, tn};
-                best_cost = cost;
-            }
-        }
+        for (int64_t s = lo; s <= hi && (s == lo || steps / s >= 4); ++s) offer(tile, s, 0, cost_of(tile, m, s));
+    }
+    if (prod != kDw && !forced_tile && ov.split_c <= 0) {
+        // whole rounds of large tiles, the rest on small ones (3 us: one more
+        // launch); 50176 x 384 -> 1024 is 6 1/8 rounds
+        const int64_t tn = ceil_div(n, dual ? kGatedBig / 2 : kGatedBig);
+        const int64_t head = ceil_div(m, kGatedBig) * tn / kNumCUs * kNumCUs / tn * kGatedBig;
+        if (head > 0 && head < m)
+            offer(kGatedBig, 1, head, cost_of(kGatedBig, head, 1) + 3.0 + cost_of(kGatedSmall, m - head, 1));
     }
     return best;
 }
@@ -265,6 +281,7 @@ const char* dt_name(int dtype) { return dtype == CNHWC_F16 ? "f16" : "bf16"; }
 
 std::string shape_name(const char* what, int dtype, const Shape& s) {
     std::string n = std::string("gated_") + what + "_" + dt_name(dtype) + "_t" + num(s.tile);
+    if (s.head) n += "+t" + num(kGatedSmall);
     if (s.splits > 1) n += "_split" + num(s.splits) + "+join";
     return n;
 }
@@ -272,15 +289,30 @@ std::string shape_name(const char* what, int dtype, const Shape& s) {
 // One product on the tiled kernel, and the join of its splits.
 int run_product(int dtype, GatedProduct prod, const Shape& s, GatedArgs a, char* ws, int64_t off_part,
                 hipStream_t st) {
-    a.tiles_m = int(s.tiles_m);
-    a.tiles_n = int(s.tiles_n);
-    a.splits = s.splits;
-    a.part = s.splits > 1 ? reinterpret_cast<float*>(ws + off_part) : nullptr;
     if (s.tiles_m * s.tiles_n > kMaxI32 / s.splits)
         return fail(CNHWC_UNSUPPORTED, "the problem needs more than 2^31 tiles");
-    int rc = launch_gated_product(dtype, prod, s.tile, a, st);
-    if (rc) return fail(rc, "launcher of the gated product refused it");
-    if ((rc = launched("gated_gemm"))) return rc;
+    a.splits = s.splits;
+    a.part = s.splits > 1 ? reinterpret_cast<float*>(ws + off_part) : nullptr;
+    auto run = [&](int tile) -> int {
+        a.tiles_m = int(ceil_div(a.m, tile));
+        a.tiles_n = int(ceil_div(a.n, prod == kProj ? tile / 2 : tile));
+        const int rc = launch_gated_product(dtype, prod, tile, a, st);
+        if (rc) return fail(rc, "launcher of the gated product refused it");
+        return launched("gated_gemm");
+    };
+    const int64_t m = a.m;
+    if (s.head) a.m = s.head;
+    int rc = run(s.tile);
+    if (rc) return rc;
+    if (s.head) {
+        // the rows behind
+        a.m = m - s.head;
+        a.a = static_cast<const char*>(a.a) + s.head * a.lda * 2;
+        if (a.y) a.y = static_cast<char*>(a.y) + s.head * a.ldy * 2;
+        if (a.dy) a.dy = static_cast<const char*>(a.dy) + s.head * a.lddy * 2;
+        if (a.dgu) a.dgu = static_cast<char*>(a.dgu) + s.head * 2 * a.fp * 2;
+        return run(kGatedSmall);
+    }
     if (s.splits > 1) {
         launch_gated_reduce(dtype, prod, a, st);
         if ((rc = launched("gated_join"))) return rc;

@@ -243,6 +243,17 @@ def test_gated_gradients_of_many_tiles(rows, c, f):
     check_gated_bwd(rows, c, f, "silu", torch.bfloat16)
 
 
+@pytest.mark.parametrize("rows,c,f,which", [(4500, 264, 2100, 0), (4480, 265, 2100, 0), (8400, 2048, 136, 1),
+                                            (8300, 2040, 72, 1)])
+def test_gated_rows_behind_whole_rounds(rows, c, f, which):
+    """The rows past the last whole round of large tiles run on small ones."""
+    x, wg = check_gated_bwd(rows, c, f, "silu", torch.float16)
+    plan = api.gated_plan(x, wg, "bwd").replace("pack ", "").split()
+    assert "+t128" in plan[which], plan
+    if which == 0:
+        check_gated_fwd(rows, c, f, "silu", torch.bfloat16)
+
+
 @pytest.mark.parametrize("rows,c,f,which", [(70, 4096, 64, 0), (66, 2049, 40, 0), (65, 64, 4096, 1), (70, 40, 2050, 1),
                                             (6000, 64, 40, 2), (5001, 72, 65, 2)])
 def test_gated_split_reductions(rows, c, f, which):

@@ -51,6 +51,10 @@ struct GatedArgs {
 constexpr int kGatedBig = 256, kGatedSmall = 128;
 
 int launch_gated_product(int dtype, GatedProduct prod, int tile, const GatedArgs& a, hipStream_t st);
+// dx and the weights' gradients on small tiles in one launch, a block a tile
+// (at most four blocks a CU), and the join of both where both are split.
+int launch_gated_pair(int dtype, const GatedArgs& dx, const GatedArgs& dw, hipStream_t st);
+int launch_gated_pair_reduce(int dtype, const GatedArgs& dx, const GatedArgs& dw, hipStream_t st);
 // Folds the partial sums of a split product into its result.
 int launch_gated_reduce(int dtype, GatedProduct prod, const GatedArgs& a, hipStream_t st);
 // Copies of up to three operands, one launch: dst [rows][ldd] = src [rows][cols]

@@ -276,14 +276,15 @@ struct Operand {
     }
 };
 
-// The kernel's arguments read again from where they were passed: what only a
-// tile's start and end need is not held in scalar registers over its steps
-// (nor anything computed from it before the loop).
+// A kernel's ARG-th argument block read again from where it was passed: what
+// only a tile's start and end need is not held in scalar registers over its
+// steps (nor anything computed from it before the loop).
 typedef const __attribute__((address_space(4))) GatedArgs ArgsMem;
+template <int ARG>
 __device__ __attribute__((always_inline)) inline ArgsMem& args_again() {
     auto p = (ArgsMem*)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(p));
-    return *p;
+    return p[ARG];
 }
 
 struct Tile {
@@ -294,9 +295,9 @@ struct Tile {
 // The v-th tile of the launch: consecutive tiles on one XCD (blocks go round
 // the 8 XCDs in turn), in groups of 8 tile rows so that the tiles at work on
 // an XCD share operands in its L2.
-template <int TILE, int NT>
+template <int TILE, int NT, int ARG>
 __device__ __attribute__((always_inline)) inline Tile tile_of(int v) {
-    ArgsMem& a = args_again();
+    ArgsMem& a = args_again<ARG>();
     const int tiles = a.tiles_m * a.tiles_n, total = tiles * a.splits;
     const int x = v & 7, base = total >> 3, rem = total & 7;
     const int id = x * base + (x < rem ? x : rem) + (v >> 3);
@@ -315,6 +316,16 @@ __device__ __attribute__((always_inline)) inline Tile tile_of(int v) {
     return t;
 }
 
+// A value that is the same in every lane, which the compiler does not always see.
+__device__ __attribute__((always_inline)) inline uint32_t uniform(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_readfirstlane(int(v)));
+}
+// A view's words for the loads written in asm.
+__device__ __attribute__((always_inline)) inline i32x4 words_of(const char* p, uint32_t n) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    return i32x4{int(uniform(uint32_t(u))), int(uniform(uint32_t(u >> 32) & 0xffffu)), int(uniform(n)), int(kRsrcWord3)};
+}
+
 __device__ __attribute__((always_inline)) inline __amdgpu_buffer_rsrc_t view(const char* p, int64_t n) {
     return make_rsrc(p, n > 0 ? (n < 0x7fffffff ? uint32_t(n) : 0x7fffffffu) : 0u);
 }
@@ -326,9 +337,15 @@ __device__ __attribute__((always_inline)) inline void store16_at(i32x4 v, __amdg
     __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
 }
 
-// END: what follows the products (a GatedEnd); ACT only where PROD is kProj.
-template <typename T, int PROD, int TILE, int END, int ACT>
-__global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_kernel(const GatedArgs a) {
+constexpr int kTileThreads(int tile) { return tile == kGatedBig ? 512 : 256; }
+constexpr int kTileLds(int tile) { return 8 * (tile / 2) * 128; }
+
+// Tiles first, first + stride, ... of one product.  END: what follows the
+// products (a GatedEnd); ACT only where PROD is kProj; ARG: which argument block
+// of the kernel.
+template <typename T, int PROD, int TILE, int END, int ACT, int ARG>
+__device__ __attribute__((always_inline)) inline void gated_product(const GatedArgs& a, unsigned char* lds,
+                                                                    const int first, const int stride) {
     constexpr bool AROWS = PROD != kDw, BROWS = PROD == kProj;
     constexpr int WN = TILE / 64;                     // waves: 2 over rows, WN over columns
     constexpr int HALF = TILE / 2;                    // rows / columns of a half tile
@@ -341,7 +358,7 @@ __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_k
     // tile's edges (the offsets past them are out of range): the waits of the
     // next tile's first step count over them
     constexpr int STORES = END == kEndPart ? 0 : PROD == kProj ? 2 * QM * (END == kEndBwd ? 2 : 1) : 4 * QM;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[8 * HBYTES];
+    static_assert(8 * HBYTES == kTileLds(TILE), "half tiles");
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -360,85 +377,107 @@ __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_k
     uint32_t so = 0;               // bytes into the rows (row operands)
     uint32_t so_step = kBK * 2;    // 0 once no tile is left: an offset past an empty view would pass its check
     const int k_end = int(a.k - int64_t(a.steps_seg - 1) * kBK);   // depth of a segment's last step
-    int cv = blockIdx.x;           // tile
+    int cv = first;                // tile
     int seg = 0, sk = 0;           // segment and step within it
     int todo = 0;                  // steps left of the tile; 0: no tile left, the views are empty
-    auto aim = [&](const Tile& t) __attribute__((always_inline)) {
-        ArgsMem& a = args_again();
-        todo = t.steps;
-        sk = t.s_lo;
-        seg = 0;
-        if (PROD == kDx && sk >= a.steps_seg) {
-            seg = 1;
-            sk -= a.steps_seg;
+    // the cursor onto the first step of tile cv.  (One closure whose two ways
+    // end in the same assignments: stores to different variables at the ends
+    // of two branches are merged into one through a pointer, and with it the
+    // cursor leaves the registers.)
+    auto aim = [&]() __attribute__((always_inline)) {
+        int t_todo = 0x7fffffff, t_sk = 0, t_seg = 0;
+        uint32_t t_so = 0, t_step = 0, t_na = 0, t_nb = 0, t_na_end = 0, t_nb_end = 0;
+        const char *t_pa = nullptr, *t_pb = nullptr, *t_pu = nullptr;
+        if (cv < total) {
+            ArgsMem& a = args_again<ARG>();
+            const Tile t = tile_of<TILE, NT, ARG>(cv);
+            t_todo = t.steps;
+            t_sk = t.s_lo;
+            if (PROD == kDx && t_sk >= a.steps_seg) {
+                t_seg = 1;
+                t_sk -= a.steps_seg;
+            }
+            const int64_t kk = int64_t(t_sk) * kBK;
+            const int64_t ktail = (PROD == kDx ? a.f : a.k) - int64_t(a.steps_seg - 1) * kBK;   // rows of the last step
+            t_so = uint32_t(kk * 2);
+            t_step = kBK * 2;
+            const char* ap = static_cast<const char*>(a.a);
+            if constexpr (AROWS) {
+                const int64_t rows = a.m - t.m0 < TILE ? a.m - t.m0 : TILE;
+                t_pa = ap + (t.m0 * a.lda + (PROD == kDx ? t_seg * a.fp : 0)) * 2;
+                // (in DX the last row of dg ends where its du begins: the mask
+                // of the reduction's end keeps every lane inside)
+                t_na = uint32_t(((rows - 1) * a.lda + a.k) * 2);
+            } else {
+                t_pa = ap + (kk * a.lda + t.m0) * 2;
+                t_na = uint32_t(kBK * a.lda * 2);
+                t_na_end = uint32_t((ktail * a.lda - t.m0) * 2);
+            }
+            if constexpr (BROWS) {
+                const int64_t rows = a.n - t.n0 < HALF ? a.n - t.n0 : HALF;
+                t_pb = static_cast<const char*>(a.b0) + t.n0 * a.ldb * 2;
+                t_pu = static_cast<const char*>(a.b1) + t.n0 * a.ldb * 2;
+                t_nb = uint32_t(((rows - 1) * a.ldb + a.k) * 2);
+            } else {
+                t_pb = static_cast<const char*>(PROD == kDx && t_seg ? a.b1 : a.b0) + (kk * a.ldb + t.n0) * 2;
+                t_nb = uint32_t(kBK * a.ldb * 2);
+                t_nb_end = uint32_t(((ktail - 1) * a.ldb + a.nb - t.n0) * 2);
+            }
         }
-        const int64_t kk = int64_t(sk) * kBK;
-        const int64_t ktail = (PROD == kDx ? a.f : a.k) - int64_t(a.steps_seg - 1) * kBK;   // rows of the last step
-        so = uint32_t(kk * 2);
-        const char* ap = static_cast<const char*>(a.a);
-        if constexpr (AROWS) {
-            const int64_t rows = a.m - t.m0 < TILE ? a.m - t.m0 : TILE;
-            pa_src = ap + (t.m0 * a.lda + (PROD == kDx ? seg * a.fp : 0)) * 2;
-            // (in DX the last row of dg ends where its du begins: the mask of
-            // the reduction's end keeps every lane inside)
-            na = uint32_t(((rows - 1) * a.lda + a.k) * 2);
-        } else {
-            pa_src = ap + (kk * a.lda + t.m0) * 2;
-            na = uint32_t(kBK * a.lda * 2);
-            na_end = uint32_t((ktail * a.lda - t.m0) * 2);
-        }
-        if constexpr (BROWS) {
-            const int64_t rows = a.n - t.n0 < HALF ? a.n - t.n0 : HALF;
-            pb_src = static_cast<const char*>(a.b0) + t.n0 * a.ldb * 2;
-            pu_src = static_cast<const char*>(a.b1) + t.n0 * a.ldb * 2;
-            nb = uint32_t(((rows - 1) * a.ldb + a.k) * 2);
-        } else {
-            pb_src = static_cast<const char*>(PROD == kDx && seg ? a.b1 : a.b0) + (kk * a.ldb + t.n0) * 2;
-            nb = uint32_t(kBK * a.ldb * 2);
-            nb_end = uint32_t(((ktail - 1) * a.ldb + a.nb - t.n0) * 2);
-        }
+        todo = t_todo;
+        sk = t_sk;
+        seg = t_seg;
+        so = t_so;
+        so_step = t_step;
+        na = t_na;
+        nb = t_nb;
+        na_end = t_na_end;
+        nb_end = t_nb_end;
+        pa_src = t_pa;
+        pb_src = t_pb;
+        pu_src = t_pu;
     };
     Load la0, la1, lb0, lb1;       // of the cursor's step; la1: of the step before
-    // (the same in every lane, which the compiler does not always see)
-    auto uni = [](uint32_t v) __attribute__((always_inline)) -> int { return __builtin_amdgcn_readfirstlane(int(v)); };
-    auto rsrc = [&](const char* p, uint32_t n) __attribute__((always_inline)) -> i32x4 {
-        const uint64_t u = reinterpret_cast<uint64_t>(p);
-        return i32x4{uni(uint32_t(u)), uni(uint32_t(u >> 32) & 0xffffu), uni(n), int(kRsrcWord3)};
-    };
-    // the cursor's loads from its state
-    auto set_a = [&](Load& l, auto hc) __attribute__((always_inline)) {
-        constexpr int h = decltype(hc)::value;
+    // one of the cursor's loads from its state
+    using LA0 = IC<0>;
+    using LA1 = IC<1>;
+    using LB0 = IC<2>;
+    using LB1 = IC<3>;
+    auto set = [&](auto wc) __attribute__((always_inline)) {
+        constexpr int W = decltype(wc)::value, h = W & 1;
         const bool last = sk == a.steps_seg - 1;
-        l.r = rsrc(pa_src, !AROWS && last ? na_end : na);
-        l.s = AROWS ? uint32_t(uni(so)) : 0u;
         const int kl = last ? k_end : kBK;
+        Load l;
+        if constexpr (W < 2) {
+            uint32_t len = na;
+            if constexpr (!AROWS) len = last ? na_end + 0u : na + 0u;   // (values, not a choice of variables)
+            l.r = words_of(pa_src, len);
+            l.s = AROWS ? uniform(so) : 0u;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) l.v[q] = !AROWS || A.lane_k[q] < kl ? A.voff[q] + h * A.half : kOob;
-    };
-    auto set_b = [&](Load& l, auto hc) __attribute__((always_inline)) {
-        constexpr int h = decltype(hc)::value;
-        const bool last = sk == a.steps_seg - 1;
-        l.r = rsrc(BROWS && h ? pu_src : pb_src, !BROWS && last ? nb_end : nb);
-        l.s = BROWS ? uint32_t(uni(so)) : 0u;
-        const int kl = last ? k_end : kBK;
+            for (int q = 0; q < 2; ++q) l.v[q] = !AROWS || A.lane_k[q] < kl ? A.voff[q] + h * A.half : kOob;
+        } else {
+            const char* src = pb_src;
+            if constexpr (BROWS && h == 1) src = pu_src;
+            uint32_t len = nb;
+            if constexpr (!BROWS) len = last ? nb_end + 0u : nb + 0u;
+            l.r = words_of(src, len);
+            l.s = BROWS ? uniform(so) : 0u;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-            l.v[q] = !BROWS || B.lane_k[q] < kl ? B.voff[q] + (BROWS ? 0 : h * B.half) : kOob;
+            for (int q = 0; q < 2; ++q)
+                l.v[q] = !BROWS || B.lane_k[q] < kl ? B.voff[q] + (BROWS ? 0 : h * B.half) : kOob;
+        }
+        if constexpr (W == 0) la0 = l;
+        else if constexpr (W == 1) la1 = l;
+        else if constexpr (W == 2) lb0 = l;
+        else lb1 = l;
     };
     // past the end of a tile or of a segment
     auto turn = [&]() __attribute__((always_inline)) {
         if (todo == 0) {
-            cv += int(gridDim.x);
-            if (cv < total) {
-                aim(tile_of<TILE, NT>(cv));
-            } else {
-                todo = 0x7fffffff;
-                sk = 0;
-                so = so_step = 0;
-                na = nb = na_end = nb_end = 0;
-            }
+            cv += stride;
+            aim();
         } else if (PROD == kDx && seg == 0 && sk == a.steps_seg) {
-            ArgsMem& a = args_again();
+            ArgsMem& a = args_again<ARG>();
             seg = 1;   // on to du and wu
             sk = 0;
             so = 0;
@@ -476,9 +515,9 @@ __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_k
         --until;
     };
     auto set_all = [&]() __attribute__((always_inline)) {
-        set_a(la0, IC<0>{});
-        set_b(lb0, IC<0>{});
-        set_b(lb1, IC<1>{});
+        set(LA0{});
+        set(LB0{});
+        set(LB1{});
     };
     auto move = [&]() __attribute__((always_inline)) {
         todo -= run;
@@ -487,7 +526,7 @@ __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_k
         if (!AROWS) pa_src += (run - 1) * (kBK * a.lda * 2);
         if (!BROWS) pb_src += (run - 1) * (kBK * a.ldb * 2);
         --sk;                      // la1: the step the cursor leaves
-        set_a(la1, IC<1>{});
+        set(LA1{});
         ++sk;
         so += so_step;
         if (!AROWS) pa_src += kBK * a.lda * 2;
@@ -618,7 +657,7 @@ __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_k
     // (the views' bases and lengths cover the rows of this tile; an offset of
     // kOob is dropped)
     auto results = [&](const Tile& t) __attribute__((always_inline)) {
-        ArgsMem& a = args_again();
+        ArgsMem& a = args_again<ARG>();
         int mrow = wm * QM * 16 + fr;                 // + half * HALF + 16 * i
         asm volatile("" : "+v"(mrow));                // offsets are not worth registers over the steps
         const int64_t mleft = a.m - t.m0;
@@ -787,8 +826,8 @@ __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_k
     };
 
     // ---- the block's tiles ----
-    Tile cur = tile_of<TILE, NT>(int(blockIdx.x));
-    aim(cur);
+    Tile cur = tile_of<TILE, NT, ARG>(first);
+    aim();
     // steps 0 and 1 but for row half 1 of step 1, which phase 0 loads
     auto load = [&](const Load& l, int at) __attribute__((always_inline)) {
         const __amdgpu_buffer_rsrc_t r = make_rsrc(
@@ -812,16 +851,41 @@ __global__ __launch_bounds__(TILE == kGatedBig ? 512 : 256, 2) void gated_gemm_k
     else read_cols<0, HB, KB>(fb0, pb);
     __builtin_amdgcn_s_barrier();
     if (PP && wm == 1) __builtin_amdgcn_s_barrier();
-    for (int v = blockIdx.x;;) {
+    for (int v = first;;) {
         step(IC<1>{});
         for (int s = 1; s < cur.steps; ++s) step(IC<0>{});
         results(cur);
-        v += int(gridDim.x);
+        v += stride;
         if (v >= total) break;
-        cur = tile_of<TILE, NT>(v);
+        cur = tile_of<TILE, NT, ARG>(v);
     }
     if (PP && wm == 0) __builtin_amdgcn_s_barrier();
     wait_vm<0>();   // the loads past the last step still write LDS
+}
+
+template <typename T, int PROD, int TILE, int END, int ACT>
+__global__ __launch_bounds__(kTileThreads(TILE), 2) void gated_gemm_kernel(const GatedArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds(TILE)];
+    gated_product<T, PROD, TILE, END, ACT, 0>(a, lds, int(blockIdx.x), int(gridDim.x));
+}
+
+// dx and the weights' gradients in one launch, where neither fills the GPU:
+// blocks below `split` take tiles of dx, the others of dwg and dwu, one tile
+// each.
+struct GatedPair {
+    GatedArgs p[2];
+    int split;
+};
+template <typename T, int END0, int END1>
+__global__ __launch_bounds__(kTileThreads(kGatedSmall), 2) void gated_pair_kernel(const GatedPair a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds(kGatedSmall)];
+    const int b = blockIdx.x;
+    if (b < a.split) {
+        if (b >= a.p[0].tiles_m * a.p[0].tiles_n * a.p[0].splits) return;
+        gated_product<T, kDx, kGatedSmall, END0, 0, 0>(a.p[0], lds, b, a.split);
+    } else {
+        gated_product<T, kDw, kGatedSmall, END1, 0, 1>(a.p[1], lds, b - a.split, int(gridDim.x) - a.split);
+    }
 }
 
 // ---- joining a split reduction: splits are added in ascending order -------------
@@ -871,7 +935,7 @@ __global__ __launch_bounds__(256) void gated_join_proj_kernel(const GatedArgs a)
 }
 
 template <typename T, bool DW>
-__global__ __launch_bounds__(256) void gated_join_kernel(const GatedArgs a) {
+__device__ __attribute__((always_inline)) inline void join_splits(const GatedArgs& a) {
     const int64_t vecs = a.part_ld / 4, n = a.m * vecs;
     for (int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x; v < n; v += int64_t(gridDim.x) * 256) {
         const int64_t m = n <= 0xffffffffll ? int64_t(uint32_t(v) / uint32_t(vecs)) : v / vecs, c = (v - m * vecs) * 4;
@@ -892,6 +956,16 @@ __global__ __launch_bounds__(256) void gated_join_kernel(const GatedArgs a) {
         for (int e = 0; e < 4; ++e)
             if (c + e < a.n) store1<T>(row + (c + e) * 2, s[e]);
     }
+}
+
+template <typename T, bool DW>
+__global__ __launch_bounds__(256) void gated_join_kernel(const GatedArgs a) {
+    join_splits<T, DW>(a);
+}
+template <typename T>
+__global__ __launch_bounds__(256) void gated_join_pair_kernel(const GatedPair a) {
+    if (blockIdx.y == 0) join_splits<T, false>(a.p[0]);
+    else join_splits<T, true>(a.p[1]);
 }
 
 // Rows copied to a wider, 16-byte-aligned stride with zeros behind them; one
@@ -966,6 +1040,15 @@ void join(GatedProduct prod, const GatedArgs& a, hipStream_t st) {
     else gated_join_kernel<T, true><<<blocks_for(a.m * (a.part_ld / 4)), 256, 0, st>>>(a);
 }
 
+template <typename T>
+void launch_pair(const GatedPair& g, int blocks, hipStream_t st) {
+    const bool p0 = g.p[0].splits > 1, p1 = g.p[1].splits > 1;
+    if (p0 && p1) gated_pair_kernel<T, kEndPart, kEndPart><<<blocks, 256, 0, st>>>(g);
+    else if (p0) gated_pair_kernel<T, kEndPart, kEndFwd><<<blocks, 256, 0, st>>>(g);
+    else if (p1) gated_pair_kernel<T, kEndFwd, kEndPart><<<blocks, 256, 0, st>>>(g);
+    else gated_pair_kernel<T, kEndFwd, kEndFwd><<<blocks, 256, 0, st>>>(g);
+}
+
 }  // namespace
 
 int launch_gated_product(int dtype, GatedProduct prod, int tile, const GatedArgs& a, hipStream_t st) {
@@ -975,6 +1058,31 @@ int launch_gated_product(int dtype, GatedProduct prod, int tile, const GatedArgs
 int launch_gated_reduce(int dtype, GatedProduct prod, const GatedArgs& a, hipStream_t st) {
     if (dtype == CNHWC_F16) join<F16>(prod, a, st);
     else join<BF16>(prod, a, st);
+    return CNHWC_OK;
+}
+
+int launch_gated_pair(int dtype, const GatedArgs& dx, const GatedArgs& dw, hipStream_t st) {
+    GatedPair g;
+    g.p[0] = dx;
+    g.p[1] = dw;
+    const int64_t n0 = int64_t(dx.tiles_m) * dx.tiles_n * dx.splits, n1 = int64_t(dw.tiles_m) * dw.tiles_n * dw.splits;
+    if (n0 + n1 > 4 * kNumCUs) return CNHWC_UNSUPPORTED;
+    g.split = int((n0 + 7) / 8 * 8);   // a multiple of the XCDs, whose tiles stay together
+    const int blocks = g.split + int(n1);
+    if (dtype == CNHWC_F16) launch_pair<F16>(g, blocks, st);
+    else launch_pair<BF16>(g, blocks, st);
+    return CNHWC_OK;
+}
+
+int launch_gated_pair_reduce(int dtype, const GatedArgs& dx, const GatedArgs& dw, hipStream_t st) {
+    GatedPair g;
+    g.p[0] = dx;
+    g.p[1] = dw;
+    g.split = 0;
+    const int64_t v0 = dx.m * (dx.part_ld / 4), v1 = dw.m * (dw.part_ld / 4);
+    const dim3 grid(blocks_for(v0 > v1 ? v0 : v1), 2);
+    if (dtype == CNHWC_F16) gated_join_pair_kernel<F16><<<grid, 256, 0, st>>>(g);
+    else gated_join_pair_kernel<BF16><<<grid, 256, 0, st>>>(g);
     return CNHWC_OK;
 }
 

@@ -187,22 +187,23 @@ struct Shape {
 // as many parts as fill the CUs.  For example 50176 x 384 -> 1024: dx on small
 // tiles 93 us, on large ones 112 us; dwg and dwu in 16 splits of the large tile
 // 99 us, unsplit on small tiles 617 us.
-Shape choose_shape(GatedProduct prod, int end, int64_t m, int64_t n, int64_t steps) {
+double tile_cost(GatedProduct prod, int end, int tile, int64_t m, int64_t n, int64_t steps, int64_t s) {
+    const bool big = tile == kGatedBig, dual = prod == kProj;
+    const int64_t tm = ceil_div(m, tile), tn = ceil_div(n, dual ? tile / 2 : tile);
+    const double step = big ? (dual ? 1.45 : 1.55) : (dual ? 0.95 : 1.0), step_alone = big ? step : 0.7;
+    const double fixed = dual ? (end == kEndBwd ? (big ? 8.0 : 4.5) : (big ? 4.0 : 2.5)) : (big ? 5.0 : 3.5);
+    const int64_t slots = big ? kNumCUs : 2 * kNumCUs;
+    const int64_t tiles = tm * tn * s, deep = ceil_div(steps, s), rest = tiles % slots;
+    double cost = double(tiles / slots) * (double(deep) * step + fixed);
+    if (rest) cost += double(deep) * (rest <= kNumCUs ? step_alone : step) + fixed;
+    if (s > 1) cost += 5.0 + double(m) * double(dual ? 2 * n : n) * double(s) * 8 / 6.0e6;
+    return cost;
+}
+
+Shape choose_shape(GatedProduct prod, int end, int64_t m, int64_t n, int64_t steps, double* cost_out = nullptr) {
     const cnhwc_override& ov = current_override();
     const bool dual = prod == kProj;
-    // unsplit, or `s` splits of it
-    auto cost_of = [&](int tile, int64_t rows, int64_t s) -> double {
-        const bool big = tile == kGatedBig;
-        const int64_t tm = ceil_div(rows, tile), tn = ceil_div(n, dual ? tile / 2 : tile);
-        const double step = big ? (dual ? 1.45 : 1.55) : (dual ? 0.95 : 1.0), step_alone = big ? step : 0.7;
-        const double fixed = dual ? (end == kEndBwd ? (big ? 8.0 : 4.5) : (big ? 4.0 : 2.5)) : (big ? 5.0 : 3.5);
-        const int64_t slots = big ? kNumCUs : 2 * kNumCUs;
-        const int64_t tiles = tm * tn * s, deep = ceil_div(steps, s), rest = tiles % slots;
-        double cost = double(tiles / slots) * (double(deep) * step + fixed);
-        if (rest) cost += double(deep) * (rest <= kNumCUs ? step_alone : step) + fixed;
-        if (s > 1) cost += 5.0 + double(rows) * double(dual ? 2 * n : n) * double(s) * 8 / 6.0e6;
-        return cost;
-    };
+    auto cost_of = [&](int tile, int64_t rows, int64_t s) { return tile_cost(prod, end, tile, rows, n, steps, s); };
     Shape best = {0, 0, 0, 0, 0};
     double best_cost = 0;
     auto offer = [&](int tile, int64_t s, int64_t head, double cost) {
@@ -225,7 +226,39 @@ Shape choose_shape(GatedProduct prod, int end, int64_t m, int64_t n, int64_t ste
         if (head > 0 && head < m)
             offer(kGatedBig, 1, head, cost_of(kGatedBig, head, 1) + 3.0 + cost_of(kGatedSmall, m - head, 1));
     }
+    if (cost_out) *cost_out = best_cost;
     return best;
+}
+
+// dx and the weights' gradients in one launch of small tiles, a block a tile:
+// the splits of both, if that is estimated faster than one after the other
+// (which costs a launch more, 4 us, and a second join).  3137 x 385 -> 1027: 68
+// -> 58 us for the whole backward pass.
+bool choose_pair(int64_t rows, int64_t c, int64_t fp, double apart, Shape* dx, Shape* dw) {
+    const cnhwc_override& ov = current_override();
+    if (ov.tune != 0 || ov.split_c != 0) return false;
+    const int64_t steps_x = 2 * ceil_div(fp, 64), steps_w = ceil_div(rows, 64);
+    const int64_t tn = ceil_div(c, kGatedSmall), mx = ceil_div(rows, kGatedSmall), mw = ceil_div(2 * fp, kGatedSmall);
+    if (mx * tn + mw * tn > 2 * kNumCUs) return false;
+    double best = apart + 4.0;
+    bool found = false;
+    for (int64_t sx = 1; sx <= 32 && (sx == 1 || steps_x / sx >= 4); ++sx)
+        for (int64_t sw = 1; sw <= 32 && (sw == 1 || steps_w / sw >= 4); ++sw) {
+            const int64_t tiles = up(mx * tn * sx, 8) + mw * tn * sw;
+            if (tiles > 2 * kNumCUs) break;
+            const double step = tiles <= kNumCUs ? 0.7 : 1.0;
+            double cost = double(std::max(ceil_div(steps_x, sx), ceil_div(steps_w, sw))) * step + 3.5;
+            if (sx > 1 || sw > 1) cost += 5.0;
+            if (sx > 1) cost += double(rows) * double(c) * double(sx) * 8 / 6.0e6;
+            if (sw > 1) cost += double(2 * fp) * double(c) * double(sw) * 8 / 6.0e6;
+            if (cost < best) {
+                best = cost;
+                found = true;
+                *dx = {kGatedSmall, int(sx), mx, tn, 0};
+                *dw = {kGatedSmall, int(sw), mw, tn, 0};
+            }
+        }
+    return found;
 }
 
 int64_t part_bytes(const Shape& s, int64_t m, int64_t ld) { return s.splits > 1 ? s.splits * m * ld * 4 : 0; }
@@ -236,6 +269,8 @@ struct GatedPlan {
     bool pack_x = false, pack_w = false;
     int64_t cp, fp;                   // c, f rounded up to multiples of 8
     Shape proj{}, dx{}, dw{};
+    bool pair = false;                // dx and dw in one launch (where both are asked for)
+    Shape pair_dx{}, pair_dw{};
     int64_t off_x = 0, off_wg = 0, off_wu = 0, off_dgu = 0, off_part = 0, bytes = 0;
 };
 
@@ -267,9 +302,14 @@ GatedPlan plan_gated(const Gated& p, int op, bool x_off, bool w_off) {
     int64_t part = part_bytes(g.proj, p.rows, 2 * g.fp);
     if (op != CNHWC_OP_FWD) {
         g.off_dgu = take(p.rows * 2 * g.fp * 2);
-        g.dx = choose_shape(kDx, kEndFwd, p.rows, p.c, 2 * ceil_div(g.fp, 64));
-        g.dw = choose_shape(kDw, kEndFwd, 2 * g.fp, p.c, ceil_div(p.rows, 64));
-        part = std::max(part, std::max(part_bytes(g.dx, p.rows, up(p.c, 4)), part_bytes(g.dw, 2 * g.fp, up(p.c, 4))));
+        double cx = 0, cw = 0;
+        g.dx = choose_shape(kDx, kEndFwd, p.rows, p.c, 2 * ceil_div(g.fp, 64), &cx);
+        g.dw = choose_shape(kDw, kEndFwd, 2 * g.fp, p.c, ceil_div(p.rows, 64), &cw);
+        g.pair = choose_pair(p.rows, p.c, g.fp, cx + cw, &g.pair_dx, &g.pair_dw);
+        const int64_t ld = up(p.c, 4);
+        part = std::max(part, std::max(part_bytes(g.dx, p.rows, ld), part_bytes(g.dw, 2 * g.fp, ld)));
+        if (g.pair)
+            part = std::max(part, up(part_bytes(g.pair_dx, p.rows, ld), 256) + part_bytes(g.pair_dw, 2 * g.fp, ld));
     }
     if (part) g.off_part = take(part);
     return g;
@@ -416,39 +456,52 @@ int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const voi
     a.part_ld = 2 * g.fp;
     a.wide = p.f % 8 == 0 && p.ys % 8 == 0 && !off16(bwd ? dy : y);
     if ((rc = run_product(p.dtype, kProj, g.proj, a, w, g.off_part, st))) return rc;
-    if (dx) {
-        GatedArgs d = a;
-        d.a = w + g.off_dgu;
-        d.lda = 2 * g.fp;
-        d.n = p.c;
-        d.k = g.fp;
-        d.nb = g.cp;
-        d.segs = 2;
-        d.steps_seg = int(ceil_div(g.fp, 64));
-        d.y = dx;
-        d.ldy = p.xs;
-        d.part_ld = up(p.c, 4);
-        d.wide = p.c % 8 == 0 && p.xs % 8 == 0 && !off16(dx);
-        if ((rc = run_product(p.dtype, kDx, g.dx, d, w, g.off_part, st))) return rc;
+    GatedArgs ax = a, aw = a;
+    ax.a = aw.a = w + g.off_dgu;
+    ax.lda = aw.lda = 2 * g.fp;
+    ax.n = aw.n = p.c;
+    ax.nb = aw.nb = g.cp;
+    ax.part_ld = aw.part_ld = up(p.c, 4);
+    // dx = [dg | du] [wg ; wu]
+    ax.k = g.fp;
+    ax.segs = 2;
+    ax.steps_seg = int(ceil_div(g.fp, 64));
+    ax.y = dx;
+    ax.ldy = p.xs;
+    ax.wide = p.c % 8 == 0 && p.xs % 8 == 0 && !off16(dx);
+    // [dwg ; dwu] = [dg | du]^T x
+    aw.b0 = xo;
+    aw.b1 = nullptr;
+    aw.ldb = ldx;
+    aw.m = 2 * g.fp;
+    aw.k = p.rows;
+    aw.steps_seg = int(ceil_div(p.rows, 64));
+    aw.y = nullptr;
+    aw.dwg = dwg;
+    aw.dwu = dwu;
+    aw.wide = p.c % 8 == 0 && !off16(dwg) && !off16(dwu);
+    if (dx && dwg && g.pair) {
+        auto set = [](GatedArgs& v, const Shape& s, float* part) {
+            v.tiles_m = int(s.tiles_m);
+            v.tiles_n = int(s.tiles_n);
+            v.splits = s.splits;
+            v.part = s.splits > 1 ? part : nullptr;
+        };
+        char* part = w + g.off_part;
+        set(ax, g.pair_dx, reinterpret_cast<float*>(part));
+        set(aw, g.pair_dw,
+            reinterpret_cast<float*>(part + up(part_bytes(g.pair_dx, p.rows, ax.part_ld), 256)));
+        if ((rc = launch_gated_pair(p.dtype, ax, aw, st))) return fail(rc, "launcher of the gated gradients refused them");
+        if ((rc = launched("gated_pair"))) return rc;
+        const bool sx = ax.splits > 1, sw = aw.splits > 1;
+        if (sx && sw) launch_gated_pair_reduce(p.dtype, ax, aw, st);
+        else if (sx) launch_gated_reduce(p.dtype, kDx, ax, st);
+        else if (sw) launch_gated_reduce(p.dtype, kDw, aw, st);
+        if ((sx || sw) && (rc = launched("gated_join"))) return rc;
+        return ok();
     }
-    if (dwg) {
-        GatedArgs d = a;
-        d.a = w + g.off_dgu;
-        d.lda = 2 * g.fp;
-        d.b0 = xo;
-        d.b1 = nullptr;
-        d.ldb = ldx;
-        d.m = 2 * g.fp;
-        d.n = p.c;
-        d.k = p.rows;
-        d.nb = g.cp;
-        d.steps_seg = int(ceil_div(p.rows, 64));
-        d.dwg = dwg;
-        d.dwu = dwu;
-        d.part_ld = up(p.c, 4);
-        d.wide = p.c % 8 == 0 && !off16(dwg) && !off16(dwu);
-        if ((rc = run_product(p.dtype, kDw, g.dw, d, w, g.off_part, st))) return rc;
-    }
+    if (dx && (rc = run_product(p.dtype, kDx, g.dx, ax, w, g.off_part, st))) return rc;
+    if (dwg && (rc = run_product(p.dtype, kDw, g.dw, aw, w, g.off_part, st))) return rc;
     return ok();
 }
 
@@ -569,7 +622,11 @@ int cnhwc_gated_plan(const cnhwc_gated_problem* prob, int op, char* name, size_t
         else {
             if (g.pack_x || g.pack_w) s = "pack ";
             s += shape_name("proj", p.dtype, g.proj);
-            if (op != CNHWC_OP_FWD) s += " " + shape_name("dx", p.dtype, g.dx) + " " + shape_name("dw", p.dtype, g.dw);
+            if (op != CNHWC_OP_FWD) {
+                const char* pair = g.pair ? "pair:" : "";
+                s += std::string(" ") + pair + shape_name("dx", p.dtype, g.pair ? g.pair_dx : g.dx);
+                s += std::string(" ") + pair + shape_name("dw", p.dtype, g.pair ? g.pair_dw : g.dw);
+            }
         }
         if (name && cap > 0) {
             std::strncpy(name, s.c_str(), cap - 1);

@@ -658,8 +658,13 @@ __device__ __attribute__((always_inline)) inline void gated_product(const GatedA
     // kOob is dropped)
     auto results = [&](const Tile& t) __attribute__((always_inline)) {
         ArgsMem& a = args_again<ARG>();
-        int mrow = wm * QM * 16 + fr;                 // + half * HALF + 16 * i
-        asm volatile("" : "+v"(mrow));                // offsets are not worth registers over the steps
+        // the lane, made anew: neither it nor what follows from it is worth
+        // registers over the steps
+        int zero = 0;
+        asm volatile("" : "+v"(zero));
+        const int lane = int(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, uint32_t(zero))));
+        const int fr = lane & 15, grp = lane >> 4;
+        const int mrow = wm * QM * 16 + fr;           // + half * HALF + 16 * i
         const int64_t mleft = a.m - t.m0;
         bool wide = a.wide != 0;   // whole 16-byte vectors, all inside or all outside the result
         if constexpr (END == kEndPart) {

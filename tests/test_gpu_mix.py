@@ -264,6 +264,23 @@ def test_gated_split_reductions(rows, c, f, which):
         check_gated_fwd(rows, c, f, "silu", torch.bfloat16)
 
 
+@pytest.mark.parametrize("rows,c,f,joins", [(129, 513, 130, ()), (300, 512, 2048, ("dx",)), (4096, 64, 64, ("dw",)),
+                                            (2000, 200, 700, ("dx", "dw")), (3137, 385, 1027, ("dx", "dw"))])
+def test_gated_gradients_in_one_launch(rows, c, f, joins):
+    """dx and the weights' gradients share a launch where neither fills the GPU; alone each has its own."""
+    t = torch.bfloat16
+    x, wg = check_gated_bwd(rows, c, f, "gelu", t)
+    plan = api.gated_plan(x, wg, "bwd").split()
+    assert {w for w in ("dx", "dw") if any(p.startswith("pair:gated_%s" % w) for p in plan)} == {"dx", "dw"}, plan
+    assert {w for w in ("dx", "dw") if any("gated_%s" % w in p and "join" in p for p in plan)} == set(joins), plan
+    (x, xr), (wg, gr), (wu, ur), (dy, dyr) = gated_operands(rows, rows, c, f, t)
+    ref, bound = mo.gated_bwd(dyr, xr, gr, ur, "gelu"), mo.gated_bwd_bound(dyr, xr, gr, ur, "gelu", t)
+    check(api.gated_bwd(dy, x, wg, wu, act="gelu", need_dw=False)[0], ref[0], bound[0], "dx")
+    got = api.gated_bwd(dy, x, wg, wu, act="gelu", need_dx=False)
+    check(got[1], ref[1], bound[1], "dwg")
+    check(got[2], ref[2], bound[2], "dwu")
+
+
 @pytest.mark.parametrize("rows,c,f,pad,shift", [(90, 64, 48, 8, 0), (90, 64, 48, 3, 0), (90, 64, 48, 0, 1),
                                                 (90, 61, 45, 5, 3), (20, 64, 48, 3, 1)])
 def test_gated_strides_and_alignment(rows, c, f, pad, shift):

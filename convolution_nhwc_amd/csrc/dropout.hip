@@ -9,6 +9,9 @@
 //
 // All 32 bits of a word decide an element: with fewer, p would be rounded (16
 // bits move p = 0.1 by 4e-6) for half the products.
+//
+// Bound by memory where large: 50176 x 384 bf16 with a residual take 19 us, 6.1
+// TB/s (two reads a write, where a copy of 1 GiB has one and reaches 5.1).
 #include "mix.h"
 
 namespace cnhwc {

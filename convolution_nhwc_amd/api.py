@@ -339,10 +339,12 @@ def _operand(t, what, f32=True):
     return dt
 
 
-def _out(t, shape, what, rows, width, ref):
-    """(output, its row stride): the caller's, or a new dense one."""
+def _out(t, what, rows, width, ref, stride, shape=None):
+    """(output, its row stride): the caller's, or a new dense one of ref's shape
+    (ref has the given row stride) or of another."""
     if t is None:
-        return ref.new_empty(shape), width
+        # (like a dense ref: that takes 0.9 us, a shape 1.5)
+        return _torch.empty_like(ref) if stride == width and shape is None else ref.new_empty(shape or ref.shape), width
     _same(t, ref, what)
     r, _, st = _rows(t, what, width)
     if r != rows:
@@ -427,11 +429,11 @@ def layernorm(x, gamma=None, beta=None, eps=1e-5, y=None):
     dt = _operand(x, "x")
     rows, c, xs = _rows(x, "x")
     pd = _ln_params(dt, gamma, beta, c, x)
-    y, ys = _out(y, x.shape, "y", rows, c, x)
+    y, ys = _out(y, "y", rows, c, x, xs)
     prob, _ = _ln_desc(rows, c, xs, ys, eps, dt, pd)
     dev = x.device
     mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = torch.empty_like(mean)
     _enqueue(lib().cnhwc_layernorm_fwd, dev, prob, _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
@@ -464,14 +466,14 @@ def layernorm_bwd(dy, x, mean, rstd, gamma=None, dx=None, param_dtype=None, ws=N
         raise ValueError("param_dtype is %s, gamma is %s" % (param_dtype, ptype))
     pd = _ln_params(dt, gamma, None, c, x) if gamma is not None else _mix_types.get(ptype, -1)
     if dx is None:
-        dx = _new_rows(x.shape, xs, x)
+        dx = _new_rows(xs, c, x)
     else:
         _same(dx, x, "dx")
         if _rows(dx, "dx", c)[::2] != (rows, xs):
             raise ValueError("dx must have x's rows and row stride (%d)" % xs)
     dev = x.device
     dgamma = x.new_empty((c,), dtype=ptype)
-    dbeta = x.new_empty((c,), dtype=ptype)
+    dbeta = torch.empty_like(dgamma)
     prob, need = _ln_desc(rows, c, xs, ys, 0.0, dt, pd)
     ws, wp, wb = _ws(ws, need, dev)
     _enqueue(lib().cnhwc_layernorm_bwd, dev, prob, _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
@@ -479,13 +481,12 @@ def layernorm_bwd(dy, x, mean, rstd, gamma=None, dx=None, param_dtype=None, ws=N
     return dx, dgamma, dbeta
 
 
-def _new_rows(shape, stride, ref):
-    """A new tensor of `shape` with the given row stride (the entry points give
-    dx the row stride of x)."""
-    c = shape[-1]
+def _new_rows(stride, c, ref):
+    """A new tensor of ref's shape with the given row stride, ref's own (the
+    entry points give dx the row stride of x)."""
     if stride == c:
-        return ref.new_empty(shape)
-    return ref.new_empty((*shape[:-1], stride))[..., :c]
+        return _torch.empty_like(ref)
+    return ref.new_empty((*ref.shape[:-1], stride))[..., :c]
 
 
 def _gated_operands(x, wg, wu, act):
@@ -535,7 +536,7 @@ def gated(x, wg, wu, act="silu", y=None, ws=None):
     """act(x wg^T) * (x wu^T) of x [..., c] and wg, wu [f, c] (or [f, 1, 1, c])."""
     _t()
     rows, c, f, xs, a, dt = _gated_operands(x, wg, wu, act)
-    y, ys = _out(y, (*x.shape[:-1], f), "y", rows, f, x)
+    y, ys = _out(y, "y", rows, f, x, xs, (*x.shape[:-1], f))
     prob, need = _gated_desc(OP_FWD, _off16(x, wg, wu), rows, c, f, xs, ys, a, dt)
     ws, wp, wb = _ws(ws, need, x.device)
     _enqueue(lib().cnhwc_gated_fwd, x.device, prob, _ptr(x), _ptr(wg), _ptr(wu), _ptr(y), wp, wb)
@@ -551,7 +552,7 @@ def gated_bwd(dy, x, wg, wu, act="silu", need_dx=True, need_dw=True, ws=None):
     drows, _, ys = _rows(dy, "dy", f)
     if drows != rows:
         raise ValueError("dy has %d rows, x has %d" % (drows, rows))
-    dx = _new_rows(x.shape, xs, x) if need_dx else None
+    dx = _new_rows(xs, c, x) if need_dx else None
     dwg = torch.empty_like(wg) if need_dw else None
     dwu = torch.empty_like(wu) if need_dw else None
     if rows or need_dw:          # an empty x has no dx to ask for
@@ -581,7 +582,7 @@ def dropout(x, p, seed, offset=0, residual=None, y=None, device_offset=None):
             raise ValueError("device_offset must hold one value")
     if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
         raise ValueError("seed and offset must be in [0, 2^64) (got %d and %d)" % (seed, offset))
-    y, ys = _out(y, x.shape, "y", rows, c, x)
+    y, ys = _out(y, "y", rows, c, x, xs)
     prob = DropoutProblem(rows, c, xs, rs, ys, p, seed, offset, dt, 0)
     _enqueue(lib().cnhwc_dropout, x.device, ctypes.byref(prob), _ptr(x), _ptr(residual), _ptr(y), _ptr(device_offset))
     return y

@@ -5,10 +5,11 @@ launched."""
 import os
 import subprocess
 
-import test_native_host as native
+import pytest
 
 
 def test_mix_host_logic_under_asan_and_ubsan():
+    native = pytest.importorskip("test_native_host")
     native._build_sanitized()        # the library's objects
     out = os.path.join(native.BUILD, "asan")
     objs = [os.path.join(out, os.path.basename(s) + ".o") for s in native._sources()]

@@ -86,10 +86,14 @@ int launch_gated_rows(int dtype, const GatedRowsArgs& a, hipStream_t st);
 // under the rounding of the 16-bit result.
 __device__ inline float sigmoid_f(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
+// max(g, 0), NaN where g is one: a single instruction (compared and selected,
+// a lane's 64 spilled their masks).
+__device__ inline float relu_f(float g) { return __builtin_elementwise_maximum(g, 0.0f); }
+
 // The normal distribution function of -|g| and, times sqrt(2 pi), its density.
 // erfc by Abramowitz and Stegun 7.1.26: a polynomial in 1 / (1 + p x) times
-// exp(-x^2), absolute error below 1.5e-7 (half that here), which is below the
-// fp32 rounding of 1 + erf; the library's erff takes about four times the
+// exp(-x^2), absolute error below 1.5e-7 (half that here; 2.4e-7 in fp32
+// arithmetic, four units of 1's last place); the library's erff takes about four times the
 // instructions, and 64 of them a lane cost a third of a 384-channel tile (this
 // one: 2.3 of its 14.4 us more than silu).
 // (Shorter forms: four coefficients reach 2e-4 relative, a logistic function of
@@ -111,10 +115,9 @@ __device__ inline float act_value(int act, float g) {
     case CNHWC_ACT_GELU: {
         // g Phi(g) = max(g, 0) - |g| Phi(-|g|)
         float e;
-        const int up = __builtin_bit_cast(int, g);   // (an integer maximum: the float one wants its operand quieted first)
-        return __builtin_fmaf(-__builtin_fabsf(g), normal_tail(g, e), __builtin_bit_cast(float, up > 0 ? up : 0));
+        return __builtin_fmaf(-__builtin_fabsf(g), normal_tail(g, e), relu_f(g));
     }
-    case CNHWC_ACT_RELU: return g < 0.0f ? 0.0f : g;   // (NaN stays)
+    case CNHWC_ACT_RELU: return relu_f(g);
     default: return sigmoid_f(g);
     }
 }
@@ -137,7 +140,7 @@ __device__ inline void act_both(int act, float g, float& v, float& d) {
         break;
     }
     case CNHWC_ACT_RELU:
-        v = g < 0.0f ? 0.0f : g;
+        v = relu_f(g);
         d = g > 0.0f ? 1.0f : 0.0f;
         break;
     default: {

@@ -785,14 +785,15 @@ __device__ __attribute__((always_inline)) inline void gated_product(const GatedA
             }
         } else {
             // rows of dx, or of dwg and then dwu; a tile of DW that holds the
-            // last rows of dwg and the first of dwu goes the narrow way
+            // last rows of dwg and the first of dwu stores in two passes
             const bool up = PROD == kDw && t.m0 >= a.fp;
+            const bool both = PROD == kDw && !up && t.m0 + TILE > a.fp;
             const int64_t r0 = up ? t.m0 - a.fp : t.m0;
             const int64_t ld = PROD == kDw ? a.n : a.ldy;
-            const int64_t rows = PROD == kDw ? a.f - r0 : mleft;
+            int64_t rows = PROD == kDw ? a.f - r0 : mleft;
             char* op = static_cast<char*>(PROD == kDx ? a.y : up ? a.dwu : a.dwg) + (r0 * ld + t.n0) * 2;
-            wide = wide && (PROD == kDx || up || t.m0 + TILE <= a.fp);
-            if (wide) {
+            int first = 0;                        // the tile's row that is the pass's row 0
+            for (;;) {
                 const __amdgpu_buffer_rsrc_t ro = view(op, ((rows - 1) * ld + a.n - t.n0) * 2);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
@@ -806,35 +807,19 @@ __device__ __attribute__((always_inline)) inline void gated_product(const GatedA
                                                                              pack2<T>(v1[0], v1[1]), false, false);
                             const auto hi = __builtin_amdgcn_permlane16_swap(pack2<T>(v0[2], v0[3]),
                                                                              pack2<T>(v1[2], v1[3]), false, false);
-                            const int ml = x * HALF + mrow + 16 * i;
+                            const i32x4 v = {int(lo[0]), int(hi[0]), int(lo[1]), int(hi[1])};
+                            const int ml = x * HALF + mrow + 16 * i - first;
                             const int c = y * HALF + wn * 32 + 16 * (grp & 1) + 8 * (grp >> 1);
-                            buf_store16(i32x4{int(lo[0]), int(hi[0]), int(lo[1]), int(hi[1])}, ro,
-                                       ml < rows && t.n0 + c < a.n ? uint32_t((ml * ld + c) * 2) : kOob);
+                            const bool in = ml >= 0 && ml < rows && t.n0 + c < a.n;
+                            if (wide) buf_store16(v, ro, in ? uint32_t((ml * ld + c) * 2) : kOob);
+                            else if (in) store_n<T>(op + (ml * ld + c) * 2, v, int(a.n - t.n0 - c < 8 ? a.n - t.n0 - c : 8));
                         }
-            } else {
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int i = 0; i < QM; ++i) {
-                        const int ml = x * HALF + mrow + 16 * i;
-                        char* row = op + ml * ld * 2;
-                        bool in = ml < mleft;
-                        if constexpr (PROD == kDw) {
-                            const int64_t m = t.m0 + ml, f = m >= a.fp ? m - a.fp : m;
-                            in = in && f < a.f;
-                            row = static_cast<char*>(m >= a.fp ? a.dwu : a.dwg) + (f * ld + t.n0) * 2;
-                        }
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int c = y * HALF + wn * 32 + 16 * j + 4 * grp;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (in && t.n0 + c + e < a.n) store1<T>(row + (c + e) * 2, acc[x][y][i][j][e]);
-                            }
-                    }
+                if (PROD != kDw || !both || first) break;
+                first = int(a.fp - t.m0);
+                rows = a.f;
+                op = static_cast<char*>(a.dwu) + t.n0 * 2;
             }
+            if (both) wide = false;               // (more stores than the next step's wait counts)
         }
         drained = !wide || STORES == 0;
         if (drained) wait_vm<0>();

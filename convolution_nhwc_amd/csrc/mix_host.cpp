@@ -181,7 +181,9 @@ struct Shape {
 // 256 x 256 tile takes 1.45 us (1.55 where an operand is read transposed), of
 // two 128 x 128 tiles sharing a CU 0.95 us (1.0), of one alone 0.7 us; a tile's
 // start and results cost `fixed` on top (the backward projections read dy and
-// write twice the forward's); partial sums move at 6 TB/s, mostly within the
+// write twice the forward's; the large tiles of the weights' gradients all store
+// at once, 73 x 3456 -> 5880 in three rounds of two steps 38 us, in five of
+// small tiles 30); partial sums move at 6 TB/s, mostly within the
 // caches, and the joining launch costs 5 us.  So small tiles win where large
 // ones leave CUs idle or the reduction is short, and a reduction is split into
 // as many parts as fill the CUs.  For example 50176 x 384 -> 1024: dx on small
@@ -191,7 +193,8 @@ double tile_cost(GatedProduct prod, int end, int tile, int64_t m, int64_t n, int
     const bool big = tile == kGatedBig, dual = prod == kProj;
     const int64_t tm = ceil_div(m, tile), tn = ceil_div(n, dual ? tile / 2 : tile);
     const double step = big ? (dual ? 1.45 : 1.55) : (dual ? 0.95 : 1.0), step_alone = big ? step : 0.7;
-    const double fixed = dual ? (end == kEndBwd ? (big ? 8.0 : 4.5) : (big ? 4.0 : 2.5)) : (big ? 5.0 : 3.5);
+    const double fixed = dual ? (end == kEndBwd ? (big ? 8.0 : 4.5) : (big ? 4.0 : 2.5)) :
+                         (big ? (prod == kDw && s == 1 ? 9.0 : 5.0) : 3.5);
     const int64_t slots = big ? kNumCUs : 2 * kNumCUs;
     const int64_t tiles = tm * tn * s, deep = ceil_div(steps, s), rest = tiles % slots;
     double cost = double(tiles / slots) * (double(deep) * step + fixed);

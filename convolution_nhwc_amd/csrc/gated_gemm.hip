@@ -42,12 +42,12 @@
 //
 // Measured, bf16 normal operands: 16384 x 2048 -> 8192 forward 780 us, 1.41
 // PFLOP/s with the activation in it (the library's product of the same flops
-// alone, 8192^3, runs at 1.39); its backward pass of 8192 rows 1260 us, 1.31
+// alone, 8192^3, runs at 1.39); its backward pass of 8192 rows 1255 us, 1.31
 // (projections 1.17, dx 1.52, weights 1.38).  The forward and dx are bound by
 // power: the matrix cores are busy 73 % of the cycles and the clock falls to
 // 1.7-1.95 GHz under them (products alone, without a load, reach 2.0 PFLOP/s).
-// With a short reduction the activation counts: 50176 x 384 -> 1024 fp16 gelu 107 us,
-// 0.74 PFLOP/s, of a tile's 14.4 us 7 for its six steps and most of the others
+// With a short reduction the activation counts: 50176 x 384 -> 1024 fp16 gelu 100 us,
+// 0.79 PFLOP/s, of a tile's 14.4 us 7 for its six steps and most of the others
 // for 64 activations a lane and their stores, which no products hide.
 #include "gated.h"
 

@@ -68,7 +68,8 @@ int launch_gated_pack(const GatedPack* p, int n, int64_t cols, int64_t ldd, hipS
 // dst[0..n) = 0 (16-bit elements)
 int launch_gated_zero(void* dst, int64_t n, hipStream_t st);
 
-// Few rows: the weights are streamed once, any strides and alignment.
+// Few rows: the weights are streamed once, any strides and alignment.  With
+// dgu: dg | du (row stride 2 fp, columns f..fp-1 zero) in the place of y.
 constexpr int kGatedFewRows = 64;
 struct GatedRowsArgs {
     const void* x;
@@ -77,8 +78,13 @@ struct GatedRowsArgs {
     void* y;
     int64_t rows, c, f, ldx, ldy;
     int act;
+    const void* dy;
+    void* dgu;
+    int64_t lddy, fp;
 };
 int launch_gated_rows(int dtype, const GatedRowsArgs& a, hipStream_t st);
+// whether x stays in registers
+bool gated_rows_kept(int64_t rows, int64_t c, bool bwd);
 
 #ifdef __HIPCC__
 

@@ -1,5 +1,6 @@
 // Gated feed-forward for few rows (decoding, small serving batches): every
-// weight is read once, so the call is bound by streaming wg and wu.
+// weight is read once, so the call is bound by streaming wg and wu.  The
+// backward pass of few rows computes its dg and du here.
 //
 // A weight tile is the 16 rows of a matrix instruction: 8 hidden units' rows
 // of wg and the same of wu, so that one instruction gives g and u of 8 units
@@ -14,7 +15,7 @@
 // blocks of one tile instead, every tile read x again through the L2, which at
 // 24 rows cost as much as the weights (2048 -> 5504 fp16: 16.8 us, of which 12.9
 // without x).  Where a wave's share of x does not fit (gated_rows_wide_kernel:
-// long rows, many of them) x is read per tile.
+// long rows) x is read per tile, which pays for up to 16 rows.
 //
 // One row, 2048 -> 8192 bf16: 12.0 us for 67 MB of weights, 5.6 TB/s.  24 rows,
 // 2048 -> 5504 fp16: 10.9 us, 4.2 TB/s; at that size a launch's start is a
@@ -52,26 +53,40 @@ __device__ __attribute__((always_inline)) inline void load_chunk(i32x4 (&r)[2], 
 }
 
 // Adds the waves' sums of one tile and stores its results.
-template <typename T, int MT, int WAVES>
+template <typename T, int MT, int WAVES, bool BWD>
 __device__ __attribute__((always_inline)) inline void finish_tile(const GatedRowsArgs& a, const float (*sums)[MT][16][17],
                                                                   int64_t tile) {
     for (int i = threadIdx.x; i < MT * 128; i += WAVES * 64) {
         const int c = i & 7, r = (i >> 3) & 15, t = i >> 7;
         const int64_t row = t * 16 + r, f = tile * 8 + c;
-        if (row < a.rows && f < a.f) {
+        if (row < a.rows && (BWD || f < a.f)) {
             float g = 0.0f, u = 0.0f;
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) {
                 g += sums[w][t][r][c];
                 u += sums[w][t][r][c + 8];
             }
-            store1<T>(static_cast<char*>(a.y) + (row * a.ldy + f) * 2, act_value(a.act, g) * u);
+            if constexpr (BWD) {
+                float dg = 0.0f, du = 0.0f;
+                if (f < a.f) {
+                    const float dy = elem<T>(load_n<T>(static_cast<const char*>(a.dy) + (row * a.lddy + f) * 2, 1), 0);
+                    float v, d;
+                    act_both(a.act, g, v, d);
+                    dg = dy * u * d;
+                    du = dy * v;
+                }
+                char* o = static_cast<char*>(a.dgu) + (row * 2 * a.fp + f) * 2;
+                store1<T>(o, dg);
+                store1<T>(o + a.fp * 2, du);
+            } else {
+                store1<T>(static_cast<char*>(a.y) + (row * a.ldy + f) * 2, act_value(a.act, g) * u);
+            }
         }
     }
 }
 
 // MT: 16-row tiles of x; NC: chunks a wave.
-template <typename T, int MT, int WAVES, int NC>
+template <typename T, int MT, int WAVES, int NC, bool BWD>
 __global__ __launch_bounds__(WAVES * 64) void gated_rows_kernel(const GatedRowsArgs a) {
     __shared__ float sums[2][WAVES][MT][16][17];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -116,13 +131,13 @@ __global__ __launch_bounds__(WAVES * 64) void gated_rows_kernel(const GatedRowsA
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-        finish_tile<T, MT, WAVES>(a, sums[buf], tile);
+        finish_tile<T, MT, WAVES, BWD>(a, sums[buf], tile);
         buf ^= 1;
     }
 }
 
 // One tile a block, x read with the weights, D chunks at a time.
-template <typename T, int MT, int WAVES, int D>
+template <typename T, int MT, int WAVES, int D, bool BWD>
 __global__ __launch_bounds__(WAVES * 64) void gated_rows_wide_kernel(const GatedRowsArgs a) {
     __shared__ float sums[WAVES][MT][16][17];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -156,40 +171,51 @@ __global__ __launch_bounds__(WAVES * 64) void gated_rows_wide_kernel(const Gated
 #pragma unroll
         for (int e = 0; e < 4; ++e) sums[wave][t][fr][4 * grp + e] = acc[t][e];
     __syncthreads();
-    finish_tile<T, MT, WAVES>(a, sums, blockIdx.x);
+    finish_tile<T, MT, WAVES, BWD>(a, sums, blockIdx.x);
 }
 
-template <typename T, int MT, int WAVES, int NC>
+constexpr int waves_of(int mt) { return mt == 4 ? 8 : 16; }
+constexpr int most_of(int mt, bool bwd) { return mt == 2 || (bwd && mt == 1) ? 2 : 4; }
+
+template <typename T, int MT, int WAVES, int NC, bool BWD>
 void launch_kept(const GatedRowsArgs& a, hipStream_t st) {
     const int64_t tiles = (a.f + 7) / 8;
     const dim3 grid((unsigned)(tiles < kNumCUs ? tiles : kNumCUs));
-    gated_rows_kernel<T, MT, WAVES, NC><<<grid, WAVES * 64, 0, st>>>(a);
+    gated_rows_kernel<T, MT, WAVES, NC, BWD><<<grid, WAVES * 64, 0, st>>>(a);
 }
 
-template <typename T, int MT>
+template <typename T, int MT, bool BWD>
 void launch(const GatedRowsArgs& a, hipStream_t st) {
     // a wave has 128 registers in a block of 16 and 256 in one of 8; its chunks
-    // of x take 8 * MT of them each, two tiles' weights 16
-    constexpr int W = MT == 4 ? 8 : 16, MOST = MT == 2 ? 2 : 4;
+    // of x take 8 * MT of them each, two tiles' weights 16 (four chunks of the
+    // backward pass spill in a block of 16)
+    constexpr int W = waves_of(MT), MOST = most_of(MT, BWD);
     const int64_t nc = ((a.c + 63) / 64 + W - 1) / W;
-    if (nc == 1) launch_kept<T, MT, W, 1>(a, st);
-    else if (nc == 2) launch_kept<T, MT, W, 2>(a, st);
-    else if (nc <= MOST) launch_kept<T, MT, W, MOST>(a, st);
-    else gated_rows_wide_kernel<T, MT, 8, MT == 1 ? 4 : MT == 2 ? 2 : 1><<<dim3((unsigned)((a.f + 7) / 8)), 512, 0, st>>>(a);
+    if (nc == 1) launch_kept<T, MT, W, 1, BWD>(a, st);
+    else if (nc == 2) launch_kept<T, MT, W, 2, BWD>(a, st);
+    else if (nc <= MOST) launch_kept<T, MT, W, MOST, BWD>(a, st);
+    else
+        gated_rows_wide_kernel<T, MT, 8, MT == 1 ? 4 : MT == 2 ? 2 : 1, BWD>
+            <<<dim3((unsigned)((a.f + 7) / 8)), 512, 0, st>>>(a);
 }
 
-template <typename T>
+template <typename T, bool BWD>
 void launch_t(const GatedRowsArgs& a, hipStream_t st) {
-    if (a.rows <= 16) launch<T, 1>(a, st);
-    else if (a.rows <= 32) launch<T, 2>(a, st);
-    else launch<T, 4>(a, st);
+    if (a.rows <= 16) launch<T, 1, BWD>(a, st);
+    else if (a.rows <= 32) launch<T, 2, BWD>(a, st);
+    else launch<T, 4, BWD>(a, st);
 }
 
 }  // namespace
 
+bool gated_rows_kept(int64_t rows, int64_t c, bool bwd) {
+    const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    return (c + 63) / 64 <= int64_t(waves_of(mt)) * most_of(mt, bwd);
+}
+
 int launch_gated_rows(int dtype, const GatedRowsArgs& a, hipStream_t st) {
-    if (dtype == CNHWC_F16) launch_t<F16>(a, st);
-    else launch_t<BF16>(a, st);
+    if (dtype == CNHWC_F16) a.dgu ? launch_t<F16, true>(a, st) : launch_t<F16, false>(a, st);
+    else a.dgu ? launch_t<BF16, true>(a, st) : launch_t<BF16, false>(a, st);
     return CNHWC_OK;
 }
 

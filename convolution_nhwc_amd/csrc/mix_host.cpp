@@ -268,7 +268,7 @@ int64_t part_bytes(const Shape& s, int64_t m, int64_t ld) { return s.splits > 1 
 
 // Everything one pass needs, with the workspace laid out.
 struct GatedPlan {
-    bool few_rows = false;            // forward on the few-rows kernel
+    bool few_rows = false;            // the projections on the few-rows kernel
     bool pack_x = false, pack_w = false;
     int64_t cp, fp;                   // c, f rounded up to multiples of 8
     Shape proj{}, dx{}, dw{};
@@ -282,14 +282,21 @@ GatedPlan plan_gated(const Gated& p, int op, bool x_off, bool w_off) {
     g.cp = up(p.c, 8);
     g.fp = up(p.f, 8);
     if (p.rows == 0) return g;
-    if (op == CNHWC_OP_FWD && p.rows <= kGatedFewRows) {
-        g.few_rows = true;
-        return g;
-    }
     // x also where a row gap would put columns past c next to a row's end:
     // those are masked, so only the 16-byte alignment of every row counts
     g.pack_x = x_off || p.xs % 8 != 0 || p.c % 8 != 0;
     g.pack_w = w_off || p.c % 8 != 0;
+    // The few-row kernel while x stays in registers (64 x 2048 -> 8192 20.3 us,
+    // 65 rows on tiles 22.6), up to one 16-row tile of x (16 x 4096 -> 8192 24.0
+    // us, on tiles 31; 32 rows 44) or where the tiles would need a copy of the
+    // weights first (64 x 2500 -> 1000 11.8 us, on tiles 21.5), which the
+    // backward pass makes in any case.
+    const bool bwd = op != CNHWC_OP_FWD;
+    g.few_rows = p.rows <= kGatedFewRows && (p.rows <= 16 || gated_rows_kept(p.rows, p.c, bwd) || (!bwd && g.pack_w));
+    if (g.few_rows && !bwd) {
+        g.pack_x = g.pack_w = false;
+        return g;
+    }
     auto take = [&](int64_t n) {
         const int64_t at = g.bytes;
         g.bytes = up(at + n, 256);
@@ -301,8 +308,11 @@ GatedPlan plan_gated(const Gated& p, int op, bool x_off, bool w_off) {
         g.off_wu = take(p.f * g.cp * 2);
     }
     const int64_t csteps = ceil_div(g.cp, 64);
-    g.proj = choose_shape(kProj, op == CNHWC_OP_FWD ? kEndFwd : kEndBwd, p.rows, p.f, csteps);
-    int64_t part = part_bytes(g.proj, p.rows, 2 * g.fp);
+    int64_t part = 0;
+    if (!g.few_rows) {
+        g.proj = choose_shape(kProj, op == CNHWC_OP_FWD ? kEndFwd : kEndBwd, p.rows, p.f, csteps);
+        part = part_bytes(g.proj, p.rows, 2 * g.fp);
+    }
     if (op != CNHWC_OP_FWD) {
         g.off_dgu = take(p.rows * 2 * g.fp * 2);
         double cx = 0, cw = 0;
@@ -410,10 +420,11 @@ int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const voi
         return ok();
     }
     if (g.few_rows) {
-        GatedRowsArgs a = {x, wg, wu, y, p.rows, p.c, p.f, p.xs, p.ys, p.act};
+        GatedRowsArgs a = {x, wg, wu, y, p.rows, p.c, p.f, p.xs, p.ys, p.act, dy,
+                           bwd ? static_cast<char*>(ws) + g.off_dgu : nullptr, p.ys, g.fp};
         launch_gated_rows(p.dtype, a, st);
         if ((rc = launched("gated_rows"))) return rc;
-        return ok();
+        if (!bwd) return ok();
     }
     char* w = static_cast<char*>(ws);
     const void *xo = x, *go = wg, *uo = wu;
@@ -458,7 +469,7 @@ int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const voi
     a.dgu = bwd ? w + g.off_dgu : nullptr;
     a.part_ld = 2 * g.fp;
     a.wide = p.f % 8 == 0 && p.ys % 8 == 0 && !off16(bwd ? dy : y);
-    if ((rc = run_product(p.dtype, kProj, g.proj, a, w, g.off_part, st))) return rc;
+    if (!g.few_rows && (rc = run_product(p.dtype, kProj, g.proj, a, w, g.off_part, st))) return rc;
     GatedArgs ax = a, aw = a;
     ax.a = aw.a = w + g.off_dgu;
     ax.lda = aw.lda = 2 * g.fp;
@@ -621,10 +632,9 @@ int cnhwc_gated_plan(const cnhwc_gated_problem* prob, int op, char* name, size_t
         const GatedPlan g = plan_gated(p, op, false, false);
         std::string s;
         if (p.rows == 0) s = "none";
-        else if (g.few_rows) s = std::string("gated_rows_") + dt_name(p.dtype);
         else {
             if (g.pack_x || g.pack_w) s = "pack ";
-            s += shape_name("proj", p.dtype, g.proj);
+            s += g.few_rows ? std::string("gated_rows_") + dt_name(p.dtype) : shape_name("proj", p.dtype, g.proj);
             if (op != CNHWC_OP_FWD) {
                 const char* pair = g.pair ? "pair:" : "";
                 s += std::string(" ") + pair + shape_name("dx", p.dtype, g.pair ? g.pair_dx : g.dx);

@@ -199,6 +199,23 @@ def test_gated_few_rows(rows, c, f, t):
     assert api.gated_plan(x, wg).startswith("gated_rows")
 
 
+@pytest.mark.parametrize("rows,c,f,rows_kernel", [(16, 4104, 40, True), (33, 2056, 72, False), (17, 2056, 65, False),
+                                                  (40, 2061, 33, True), (64, 2048, 24, True)])
+def test_gated_few_rows_of_many_channels(rows, c, f, rows_kernel):
+    """Where x does not stay in registers: one 16-row tile, operands that tiles would copy first."""
+    x, wg = check_gated_fwd(rows, c, f, "silu", torch.bfloat16)
+    assert api.gated_plan(x, wg).startswith("gated_rows") == rows_kernel
+
+
+@pytest.mark.parametrize("rows,c,f,rows_kernel", [
+    (1, 1, 1, True), (1, 2048, 300, True), (9, 2049, 17, True), (16, 4200, 40, True), (17, 65, 33, True),
+    (32, 2040, 100, True), (32, 2056, 48, False), (50, 2048, 20, True), (64, 520, 49, True), (60, 2056, 24, False)])
+@pytest.mark.parametrize("name", ["silu", "relu"])
+def test_gated_backward_projections_of_few_rows(rows, c, f, rows_kernel, name):
+    x, wg = check_gated_bwd(rows, c, f, name, torch.float16)
+    assert ("gated_rows" in api.gated_plan(x, wg, "bwd")) == rows_kernel
+
+
 @pytest.mark.parametrize("name", sorted(api.ACTS))
 def test_gated_activations(name):
     check_gated_fwd(9, 72, 40, name, torch.float16)

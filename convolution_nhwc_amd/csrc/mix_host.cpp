@@ -290,9 +290,10 @@ GatedPlan plan_gated(const Gated& p, int op, bool x_off, bool w_off) {
     // 65 rows on tiles 22.6), up to one 16-row tile of x (16 x 4096 -> 8192 24.0
     // us, on tiles 31; 32 rows 44) or where the tiles would need a copy of the
     // weights first (64 x 2500 -> 1000 11.8 us, on tiles 21.5), which the
-    // backward pass makes in any case.
+    // backward pass makes in any case.  (By c alone, not by the pointers: the
+    // workspace for any pointers has to do for aligned ones.)
     const bool bwd = op != CNHWC_OP_FWD;
-    g.few_rows = p.rows <= kGatedFewRows && (p.rows <= 16 || gated_rows_kept(p.rows, p.c, bwd) || (!bwd && g.pack_w));
+    g.few_rows = p.rows <= kGatedFewRows && (p.rows <= 16 || gated_rows_kept(p.rows, p.c, bwd) || (!bwd && p.c % 8 != 0));
     if (g.few_rows && !bwd) {
         g.pack_x = g.pack_w = false;
         return g;

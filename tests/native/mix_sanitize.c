@@ -79,7 +79,7 @@ static void refusals(void) {
     EXPECT(cnhwc_layernorm_fwd(&ln, b, NULL, NULL, b + 62, mean, rstd, NULL) == CNHWC_INVALID_ARG, "y over x");
     EXPECT(cnhwc_layernorm_bwd(&ln, b, b + 512, NULL, mean, rstd, NULL, NULL, NULL, NULL, 0, NULL) ==
            CNHWC_INVALID_ARG, "nothing to compute");
-    EXPECT(cnhwc_layernorm_bwd(&ln, b, b + 512, NULL, mean, rstd, b + 1024, b + 2048, b + 3072, b + 16384, 1, NULL) ==
+    EXPECT(cnhwc_layernorm_bwd(&ln, b, b + 512, NULL, mean, rstd, b + 1024, b + 2048, b + 2560, b + 16384, 1, NULL) ==
            CNHWC_WORKSPACE_TOO_SMALL, "short workspace");
     cnhwc_gated_problem g;
     memset(&g, 0, sizeof g);

@@ -119,9 +119,12 @@ __device__ inline float act_value(int act, float g) {
     switch (act) {
     case CNHWC_ACT_SILU: return g * sigmoid_f(g);
     case CNHWC_ACT_GELU: {
-        // g Phi(g) = max(g, 0) - |g| Phi(-|g|)
-        float e;
-        return __builtin_fmaf(-__builtin_fabsf(g), normal_tail(g, e), relu_f(g));
+        // g Phi(g) = max(g, 0) - |g| Phi(-|g|).  Phi(-16) is 0 in fp32, so the
+        // factor of the tail stops there for positive g: at +inf, inf * 0 would
+        // be NaN where the value is inf.
+        float e, q = normal_tail(g, e);
+        asm("" : "+v"(g), "+v"(q));   // the rest after the tail: a lane's 64 minima ahead of their use spill
+        return __builtin_fmaf(-__builtin_fabsf(__builtin_elementwise_minimum(g, 16.0f)), q, relu_f(g));
     }
     case CNHWC_ACT_RELU: return relu_f(g);
     default: return sigmoid_f(g);

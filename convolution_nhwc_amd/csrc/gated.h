@@ -157,9 +157,12 @@ __device__ inline void act_both(int act, float g, float& v, float& d) {
         d = g > 0.0f ? 1.0f : 0.0f;
         break;
     default: {
-        const float s = sigmoid_f(g);
-        v = s;
-        d = s * (1.0f - s);
+        // s (1 - s) by exp(-|g|): the difference loses its bits where s nears 1
+        // (half a percent of the slope at g = 12, all of it past 17)
+        const float e = __expf(-__builtin_fabsf(g)), r = __builtin_amdgcn_rcpf(1.0f + e);
+        const float q = e * r;
+        v = g >= 0.0f ? r : q;
+        d = q * r;
     }
     }
 }

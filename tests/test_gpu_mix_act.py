@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 TYPES = mo.TYPES
 NAMES = sorted(api.ACTS)
-SWEPT = ["gelu"]
+SWEPT = ["gelu", "sigmoid"]
 
 
 def check(got, ref, bound, what):

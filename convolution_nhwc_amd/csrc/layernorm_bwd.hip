@@ -83,7 +83,8 @@ __global__ __launch_bounds__(L > 256 ? L : 256) void ln_bwd_kernel(const LnArgs 
         float g[NV][V];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            // (columns past c hold dy = 0, which adds nothing to any sum)
+            // (columns past c hold dy = 0, which adds nothing to any sum while
+            // mean * rstd is finite)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float d = elem<T>(dy[i], e), xh = (elem<T>(x[i], e) - mean) * rstd;
@@ -95,6 +96,15 @@ __global__ __launch_bounds__(L > 256 ? L : 256) void ln_bwd_kernel(const LnArgs 
                     db[i][e] += d;
                 }
             }
+        }
+        if (!(__builtin_fabsf(mean * rstd) < __builtin_inff())) {
+            // x - mean may be small all the same: the row's own columns alone
+            s2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if ((i * L + li) * V + e < a.c) s2 += g[i][e] * ((elem<T>(x[i], e) - mean) * rstd);
         }
         row_sum2<L>(s1, s2, red, phase);
         const float m1 = s1 / a.cf, m2 = s2 / a.cf;

@@ -1,0 +1,38 @@
+"""Calls at the edges of the channel-mixing operators: what the ordinary tests'
+sizes, values and arguments do not reach."""
+import pytest
+import torch
+
+import mix_oracle as mo
+from convolution_nhwc_amd import api
+
+pytestmark = pytest.mark.gpu
+
+TYPES = mo.TYPES
+
+
+def rnd(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("c", [1, 8, 24, 70, 385, 1537, 2056, 5001, 9000, 20001])
+def test_layernorm_backward_of_constant_rows_far_from_zero(c, t):
+    """mean * rstd is past fp32's largest value, (x - mean) * rstd is 0: lanes without a column
+    must not bring the former into the row's sums."""
+    t = TYPES[t]
+    rows, big, rstd = 21, 2.0 ** 110, 2.0 ** 20
+    x = torch.full((rows, c), big, dtype=t)
+    mean, r = torch.full((rows,), big), torch.full((rows,), rstd)
+    dy = rnd(c, rows, c).to(t)
+    g = dy.double()
+    dx, dgamma, dbeta = api.layernorm_bwd(dy.cuda(), x.cuda(), mean.cuda(), r.cuda())
+    m1 = g.mean(1, keepdim=True)
+    ref = rstd * (g - m1)
+    size = g.abs().mean(1, keepdim=True)
+    # m1 by a sum of c terms and a division, the difference and the product
+    bound = mo.half_step(t, ref) + rstd * (mo.chain(c) * size + 4 * mo.U32 * (g.abs() + size))
+    assert bool(((dx.double().cpu() - ref).abs() <= bound).all())
+    assert bool((dgamma == 0).all())
+    sums = mo.half_step(t, g.sum(0)) + mo.chain(rows) * g.abs().sum(0)
+    assert bool(((dbeta.double().cpu() - g.sum(0)).abs() <= sums).all())

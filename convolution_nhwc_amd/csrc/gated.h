@@ -52,7 +52,8 @@ constexpr int kGatedBig = 256, kGatedSmall = 128;
 
 int launch_gated_product(int dtype, GatedProduct prod, int tile, const GatedArgs& a, hipStream_t st);
 // dx and the weights' gradients on small tiles in one launch, a block a tile
-// (at most four blocks a CU), and the join of both where both are split.
+// (at most two blocks a CU, what its LDS takes), and the join of both where both
+// are split.
 int launch_gated_pair(int dtype, const GatedArgs& dx, const GatedArgs& dw, hipStream_t st);
 int launch_gated_pair_reduce(int dtype, const GatedArgs& dx, const GatedArgs& dw, hipStream_t st);
 // Folds the partial sums of a split product into its result.
@@ -82,6 +83,8 @@ struct GatedRowsArgs {
     void* dgu;
     int64_t lddy, fp;
 };
+// (CNHWC_UNSUPPORTED: more than 16 rows of dg and du whose x does not stay in
+// registers)
 int launch_gated_rows(int dtype, const GatedRowsArgs& a, hipStream_t st);
 // whether x stays in registers
 bool gated_rows_kept(int64_t rows, int64_t c, bool bwd);

@@ -1066,8 +1066,8 @@ int launch_gated_pair(int dtype, const GatedArgs& dx, const GatedArgs& dw, hipSt
     g.p[0] = dx;
     g.p[1] = dw;
     const int64_t n0 = int64_t(dx.tiles_m) * dx.tiles_n * dx.splits, n1 = int64_t(dw.tiles_m) * dw.tiles_n * dw.splits;
-    if (n0 + n1 > 4 * kNumCUs) return CNHWC_UNSUPPORTED;
     g.split = int((n0 + 7) / 8 * 8);   // a multiple of the XCDs, whose tiles stay together
+    if (g.split + n1 > 2 * kNumCUs) return CNHWC_UNSUPPORTED;
     const int blocks = g.split + int(n1);
     if (dtype == CNHWC_F16) launch_pair<F16>(g, blocks, st);
     else launch_pair<BF16>(g, blocks, st);

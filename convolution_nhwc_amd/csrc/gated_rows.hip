@@ -178,32 +178,37 @@ constexpr int waves_of(int mt) { return mt == 4 ? 8 : 16; }
 constexpr int most_of(int mt, bool bwd) { return mt == 2 || (bwd && mt == 1) ? 2 : 4; }
 
 template <typename T, int MT, int WAVES, int NC, bool BWD>
-void launch_kept(const GatedRowsArgs& a, hipStream_t st) {
+int launch_kept(const GatedRowsArgs& a, hipStream_t st) {
     const int64_t tiles = (a.f + 7) / 8;
     const dim3 grid((unsigned)(tiles < kNumCUs ? tiles : kNumCUs));
     gated_rows_kernel<T, MT, WAVES, NC, BWD><<<grid, WAVES * 64, 0, st>>>(a);
+    return CNHWC_OK;
 }
 
 template <typename T, int MT, bool BWD>
-void launch(const GatedRowsArgs& a, hipStream_t st) {
+int launch(const GatedRowsArgs& a, hipStream_t st) {
     // a wave has 128 registers in a block of 16 and 256 in one of 8; its chunks
     // of x take 8 * MT of them each, two tiles' weights 16 (four chunks of the
     // backward pass spill in a block of 16)
     constexpr int W = waves_of(MT), MOST = most_of(MT, BWD);
     const int64_t nc = ((a.c + 63) / 64 + W - 1) / W;
-    if (nc == 1) launch_kept<T, MT, W, 1, BWD>(a, st);
-    else if (nc == 2) launch_kept<T, MT, W, 2, BWD>(a, st);
-    else if (nc <= MOST) launch_kept<T, MT, W, MOST, BWD>(a, st);
-    else
+    if (nc == 1) return launch_kept<T, MT, W, 1, BWD>(a, st);
+    if (nc == 2) return launch_kept<T, MT, W, 2, BWD>(a, st);
+    if (nc <= MOST) return launch_kept<T, MT, W, MOST, BWD>(a, st);
+    if constexpr (BWD && MT > 1) {
+        return CNHWC_UNSUPPORTED;   // these go to the tiles: the weights' copy is made for them in any case
+    } else {
         gated_rows_wide_kernel<T, MT, 8, MT == 1 ? 4 : MT == 2 ? 2 : 1, BWD>
             <<<dim3((unsigned)((a.f + 7) / 8)), 512, 0, st>>>(a);
+        return CNHWC_OK;
+    }
 }
 
 template <typename T, bool BWD>
-void launch_t(const GatedRowsArgs& a, hipStream_t st) {
-    if (a.rows <= 16) launch<T, 1, BWD>(a, st);
-    else if (a.rows <= 32) launch<T, 2, BWD>(a, st);
-    else launch<T, 4, BWD>(a, st);
+int launch_t(const GatedRowsArgs& a, hipStream_t st) {
+    if (a.rows <= 16) return launch<T, 1, BWD>(a, st);
+    if (a.rows <= 32) return launch<T, 2, BWD>(a, st);
+    return launch<T, 4, BWD>(a, st);
 }
 
 }  // namespace
@@ -214,9 +219,8 @@ bool gated_rows_kept(int64_t rows, int64_t c, bool bwd) {
 }
 
 int launch_gated_rows(int dtype, const GatedRowsArgs& a, hipStream_t st) {
-    if (dtype == CNHWC_F16) a.dgu ? launch_t<F16, true>(a, st) : launch_t<F16, false>(a, st);
-    else a.dgu ? launch_t<BF16, true>(a, st) : launch_t<BF16, false>(a, st);
-    return CNHWC_OK;
+    if (dtype == CNHWC_F16) return a.dgu ? launch_t<F16, true>(a, st) : launch_t<F16, false>(a, st);
+    return a.dgu ? launch_t<BF16, true>(a, st) : launch_t<BF16, false>(a, st);
 }
 
 }  // namespace cnhwc

@@ -423,7 +423,7 @@ int run_gated(const cnhwc_gated_problem* prob, int op, const void* dy, const voi
     if (g.few_rows) {
         GatedRowsArgs a = {x, wg, wu, y, p.rows, p.c, p.f, p.xs, p.ys, p.act, dy,
                            bwd ? static_cast<char*>(ws) + g.off_dgu : nullptr, p.ys, g.fp};
-        launch_gated_rows(p.dtype, a, st);
+        if ((rc = launch_gated_rows(p.dtype, a, st))) return fail(rc, "launcher of the few-row product refused it");
         if ((rc = launched("gated_rows"))) return rc;
         if (!bwd) return ok();
     }

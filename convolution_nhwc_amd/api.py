@@ -14,6 +14,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcnhwc.so")
@@ -187,15 +188,22 @@ def cnhwc_wgrad(p, x, dy, dw, ws, ws_bytes, stream):
     _check(lib().cnhwc_wgrad(ctypes.byref(_problem(p)), x, dy, dw, ws, ws_bytes, stream))
 
 
+class _Forced(threading.local):
+    key = None   # what of this thread's override decides the gated product's sizes
+
+
+_forced = _Forced()
+
+
 def cnhwc_set_override(variant=0, cpl=0, split_c=0, chunk_limit_bytes=0, tune=0):
-    _gated_desc.cache_clear()
     _check(lib().cnhwc_set_override(ctypes.byref(Override(variant, cpl, split_c, tune,
                                                           chunk_limit_bytes))))
+    _forced.key = (split_c, tune)
 
 
 def cnhwc_clear_override():
-    _gated_desc.cache_clear()
     _check(lib().cnhwc_set_override(None))
+    _forced.key = None
 
 
 @contextlib.contextmanager
@@ -389,7 +397,7 @@ def _enqueue(fn, device, *args):
 
 
 # Descriptors and workspace sizes by their fields (a model calls few shapes
-# often); dropped when the test override changes, which sizes depend on.
+# often), and by what of the thread's test override sizes depend on.
 
 @functools.lru_cache(maxsize=1024)
 def _ln_desc(*fields):
@@ -401,7 +409,7 @@ def _ln_desc(*fields):
 
 
 @functools.lru_cache(maxsize=1024)
-def _gated_desc(op, unaligned, *fields):
+def _gated_desc(forced, op, unaligned, *fields):
     """(descriptor reference, workspace bytes)"""
     prob = GatedProblem(*fields, 0)
     b = ctypes.c_size_t()
@@ -519,7 +527,7 @@ def gated_workspace(x, wg, which="fwd"):
     if which not in ("fwd", "bwd"):
         raise ValueError('which must be "fwd" or "bwd" (got %r)' % (which,))
     rows, c, f, xs, a, dt = _gated_operands(x, wg, wg, "silu")
-    return _gated_desc(OP_FWD if which == "fwd" else OP_DGRAD, _off16(x, wg), rows, c, f, xs, 0, a, dt)[1]
+    return _gated_desc(_forced.key, OP_FWD if which == "fwd" else OP_DGRAD, _off16(x, wg), rows, c, f, xs, 0, a, dt)[1]
 
 
 def gated_plan(x, wg, which="fwd"):
@@ -537,7 +545,7 @@ def gated(x, wg, wu, act="silu", y=None, ws=None):
     _t()
     rows, c, f, xs, a, dt = _gated_operands(x, wg, wu, act)
     y, ys = _out(y, "y", rows, f, x, xs, (*x.shape[:-1], f))
-    prob, need = _gated_desc(OP_FWD, _off16(x, wg, wu), rows, c, f, xs, ys, a, dt)
+    prob, need = _gated_desc(_forced.key, OP_FWD, _off16(x, wg, wu), rows, c, f, xs, ys, a, dt)
     ws, wp, wb = _ws(ws, need, x.device)
     _enqueue(lib().cnhwc_gated_fwd, x.device, prob, _ptr(x), _ptr(wg), _ptr(wu), _ptr(y), wp, wb)
     return y
@@ -556,7 +564,7 @@ def gated_bwd(dy, x, wg, wu, act="silu", need_dx=True, need_dw=True, ws=None):
     dwg = torch.empty_like(wg) if need_dw else None
     dwu = torch.empty_like(wu) if need_dw else None
     if rows or need_dw:          # an empty x has no dx to ask for
-        prob, need = _gated_desc(OP_DGRAD, _off16(x, wg, wu), rows, c, f, xs, ys, a, dt)
+        prob, need = _gated_desc(_forced.key, OP_DGRAD, _off16(x, wg, wu), rows, c, f, xs, ys, a, dt)
         ws, wp, wb = _ws(ws, need, x.device)
         _enqueue(lib().cnhwc_gated_bwd, x.device, prob, _ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(dx), _ptr(dwg),
                  _ptr(dwu), wp, wb)

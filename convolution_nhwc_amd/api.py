@@ -520,14 +520,18 @@ def _off16(*tensors):
     return 0
 
 
-def gated_workspace(x, wg, which="fwd"):
+def gated_workspace(x, wg, which="fwd", wu=None):
     """Workspace bytes of gated (which="fwd") or gated_bwd ("bwd") for operands
-    like x and wg."""
+    like x, wg and wu.  Without wu it is taken to be aligned as wg is (the copies
+    of weights off a 16-byte boundary lie in the workspace)."""
     _t()
     if which not in ("fwd", "bwd"):
         raise ValueError('which must be "fwd" or "bwd" (got %r)' % (which,))
-    rows, c, f, xs, a, dt = _gated_operands(x, wg, wg, "silu")
-    return _gated_desc(_forced.key, OP_FWD if which == "fwd" else OP_DGRAD, _off16(x, wg), rows, c, f, xs, 0, a, dt)[1]
+    if wu is None:
+        wu = wg
+    rows, c, f, xs, a, dt = _gated_operands(x, wg, wu, "silu")
+    op = OP_FWD if which == "fwd" else OP_DGRAD
+    return _gated_desc(_forced.key, op, _off16(x, wg, wu), rows, c, f, xs, 0, a, dt)[1]
 
 
 def gated_plan(x, wg, which="fwd"):

@@ -36,3 +36,22 @@ def test_layernorm_backward_of_constant_rows_far_from_zero(c, t):
     assert bool((dgamma == 0).all())
     sums = mo.half_step(t, g.sum(0)) + mo.chain(rows) * g.abs().sum(0)
     assert bool(((dbeta.double().cpu() - g.sum(0)).abs() <= sums).all())
+
+
+@pytest.mark.parametrize("rows", [9, 90])
+def test_gated_workspace_of_weights_apart(rows):
+    """wu off a 16-byte boundary beside an aligned wg, as in one buffer of many weights."""
+    t = torch.bfloat16
+    c, f = 64, 40
+    x = rnd(1, rows, c).to(t).cuda()
+    flat = torch.empty(2 * f * c + 3, dtype=t, device="cuda")
+    wg, wu = flat[:f * c].view(f, c), flat[f * c + 3:].view(f, c)
+    wg.copy_(rnd(2, f, c))
+    wu.copy_(rnd(3, f, c))
+    dy = rnd(4, rows, f).to(t).cuda()
+    same = wu.clone()
+    for which, call in (("fwd", lambda u, ws: (api.gated(x, wg, u, ws=ws),)),
+                        ("bwd", lambda u, ws: api.gated_bwd(dy, x, wg, u, ws=ws))):
+        ws = torch.empty(api.gated_workspace(x, wg, which, wu), dtype=torch.uint8, device="cuda")
+        for got, want in zip(call(wu, ws), call(same, None)):
+            assert torch.equal(got, want)

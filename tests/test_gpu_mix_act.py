@@ -6,13 +6,13 @@ import torch
 
 import mix_act as ma
 import mix_oracle as mo
+import test_gpu_mix as tm
 from convolution_nhwc_amd import api
 
 pytestmark = pytest.mark.gpu
 
 TYPES = mo.TYPES
 NAMES = sorted(api.ACTS)
-SWEPT = ["gelu", "sigmoid"]
 
 
 def check(got, ref, bound, what):
@@ -44,14 +44,14 @@ def sweep(name, t, rows, c, f, kernel, kernel_bwd=None):
         check(got, r, b, n)
 
 
-@pytest.mark.parametrize("name", SWEPT)
+@pytest.mark.parametrize("name", NAMES)
 @pytest.mark.parametrize("t", ["f16", "bf16"])
 @pytest.mark.parametrize("rows,c,f", [(1, 8, 4096), (20, 136, 4095), (64, 72, 2048)])
 def test_few_rows(rows, c, f, t, name):
     sweep(name, t, rows, c, f, "gated_rows")
 
 
-@pytest.mark.parametrize("name", SWEPT)
+@pytest.mark.parametrize("name", NAMES)
 @pytest.mark.parametrize("t", ["f16", "bf16"])
 @pytest.mark.parametrize("tile,rows,c,f", [
     # more tiles than blocks, so that a tile's stores are in flight in the next
@@ -62,12 +62,23 @@ def test_tiles(tile, rows, c, f, t, name):
         sweep(name, t, rows, c, f, "_t%d" % tile)
 
 
-@pytest.mark.parametrize("name", SWEPT)
+@pytest.mark.parametrize("name", NAMES)
 @pytest.mark.parametrize("t", ["f16", "bf16"])
 @pytest.mark.parametrize("tile", [128, 256])
 def test_joined_splits(tile, t, name):
     with api.override(tune=tile, split_c=3):
         sweep(name, t, 70, 200, 2050, "split3")
+
+
+@pytest.mark.parametrize("rows,c,f", [(4000, 200, 2100), (600, 136, 1027)])
+@pytest.mark.parametrize("name", NAMES)
+def test_large_tile_with_cut_vectors(rows, c, f, name):
+    """Random fp16 operands on the 256 tile where f is no multiple of 8."""
+    with api.override(tune=256, split_c=1):
+        x, wg = tm.check_gated_fwd(rows, c, f, name, torch.float16)
+        assert api.gated_plan(x, wg) == "gated_proj_f16_t256"
+        x, wg = tm.check_gated_bwd(rows, c, f, name, torch.float16)
+        assert api.gated_plan(x, wg, "bwd").count("_t256") == 3
 
 
 # ---- pre-activations that overflow ------------------------------------------------

@@ -1,5 +1,7 @@
 """Calls at the edges of the channel-mixing operators: what the ordinary tests'
 sizes, values and arguments do not reach."""
+import ctypes
+
 import pytest
 import torch
 
@@ -55,3 +57,22 @@ def test_gated_workspace_of_weights_apart(rows):
         ws = torch.empty(api.gated_workspace(x, wg, which, wu), dtype=torch.uint8, device="cuda")
         for got, want in zip(call(wu, ws), call(same, None)):
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,c", [(1, 1), (37, 70), (300, 384), (5, 2056), (3, 9000), (2, 40000)])
+def test_layernorm_without_statistics(rows, c, t):
+    """mean, rstd or both NULL: y has the same bits, and the statistic that is asked for too."""
+    code, t = {"f16": api.F16, "bf16": api.BF16, "f32": api.F32}[t], TYPES[t]
+    x, gamma, beta = (rnd(i, *s).to(t).cuda() for i, s in enumerate(((rows, c), (c,), (c,))))
+    want = api.layernorm(x, gamma, beta)
+    q = api.LayernormProblem(rows, c, 0, 0, 1e-5, code, code, 0)
+    for asked in ((0, 0), (1, 0), (0, 1)):
+        y = torch.full_like(x, float("nan"))
+        stats = [torch.full((rows,), float("nan"), device="cuda") for _ in range(2)]
+        api._check(api.lib().cnhwc_layernorm_fwd(
+            ctypes.byref(q), x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), y.data_ptr(),
+            *(s.data_ptr() if a else None for s, a in zip(stats, asked)), torch.cuda.current_stream().cuda_stream))
+        assert torch.equal(y, want[0]), asked
+        for s, a, w in zip(stats, asked, want[1:]):
+            assert torch.equal(s, w) if a else bool(s.isnan().all()), asked

@@ -99,7 +99,7 @@ __device__ inline float sigmoid_f(float g) { return __builtin_amdgcn_rcpf(1.0f +
 // a lane's 64 spilled their masks).
 __device__ inline float relu_f(float g) { return __builtin_elementwise_maximum(g, 0.0f); }
 
-// The normal distribution function of -|g| and, times sqrt(2 pi), its density.
+// The normal distribution function of -|g|, and times sqrt(2 pi) its density.
 // Phi(-a) = exp(-a^2 / 2) t P(t) with t = 1 / (1 + 0.3 a), where erfcx's slow
 // fall is nearly a polynomial in t.  P has six terms, fitted by linear
 // programming to the least e with an error below e relative to Phi and below
@@ -110,6 +110,8 @@ __device__ inline float relu_f(float g) { return __builtin_elementwise_maximum(g
 // 2.5e-6, seven 2.1e-6 and 6e-8 for one instruction more; the library's erff
 // takes about four times the instructions, and 64 of them a lane cost a third
 // of a 384-channel tile.
+//
+// Returned as q and e = exp(-a^2 / 2), with Phi(-a) = e q.
 __device__ inline float normal_tail(float g, float& e) {
     e = __builtin_amdgcn_exp2f(g * g * (-0.5f * 1.44269504088896341f));
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, __builtin_fabsf(g), 1.0f));
@@ -118,20 +120,23 @@ __device__ inline float normal_tail(float g, float& e) {
     q = __builtin_fmaf(q, t, 0.1478436f);
     q = __builtin_fmaf(q, t, 0.11291612f);
     q = __builtin_fmaf(q, t, 0.12014362f);
-    return q * t * e;
+    return q * t;
 }
+// a * b, and 0 where one of them is 0 whatever the other: gelu's products with
+// its tail and density, which have fallen to 0 long before g is infinite (inf *
+// 0 is NaN, where gelu's value and slope have limits).  v_mul_legacy_f32, which
+// the compiler has as an intrinsic without a builtin's name.
+__device__ float mul_0(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
 
 // act(g)
 __device__ inline float act_value(int act, float g) {
     switch (act) {
     case CNHWC_ACT_SILU: return g * sigmoid_f(g);
     case CNHWC_ACT_GELU: {
-        // g Phi(g) = max(g, 0) - |g| Phi(-|g|).  Phi(-16) is 0 in fp32, so the
-        // factor of the tail stops there for positive g: at +inf, inf * 0 would
-        // be NaN where the value is inf.
-        float e, q = normal_tail(g, e);
-        asm("" : "+v"(g), "+v"(q));   // the rest after the tail: a lane's 64 minima ahead of their use spill
-        return __builtin_fmaf(-__builtin_fabsf(__builtin_elementwise_minimum(g, 16.0f)), q, relu_f(g));
+        // g Phi(g) = max(g, 0) - |g| Phi(-|g|)
+        float e;
+        const float q = normal_tail(g, e);
+        return __builtin_fmaf(-__builtin_fabsf(mul_0(g, e)), q, relu_f(g));
     }
     case CNHWC_ACT_RELU: return relu_f(g);
     default: return sigmoid_f(g);
@@ -149,10 +154,10 @@ __device__ inline void act_both(int act, float g, float& v, float& d) {
     }
     case CNHWC_ACT_GELU: {
         float e;
-        const float q = normal_tail(g, e);
+        const float q = normal_tail(g, e) * e;
         const float c = g >= 0.0f ? 1.0f - q : q;
-        v = g * c;
-        d = c + g * (e * 0.39894228040143268f);
+        v = mul_0(g, c);
+        d = __builtin_fmaf(mul_0(g, e), 0.39894228040143268f, c);
         break;
     }
     case CNHWC_ACT_RELU:

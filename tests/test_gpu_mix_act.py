@@ -84,8 +84,8 @@ def test_large_tile_with_cut_vectors(rows, c, f, name):
 # ---- pre-activations that overflow ------------------------------------------------
 
 INF = float("inf")
-# act(+inf); act(-inf) where the formula has a value there (silu and gelu: -inf * 0)
-AT_INF = {"silu": (INF, None), "gelu": (INF, None), "relu": (INF, 0.0), "sigmoid": (1.0, 0.0)}
+# act(+inf); act(-inf) (None: not tested, the formula is -inf * 0)
+AT_INF = {"silu": (INF, None), "gelu": (INF, 0.0), "relu": (INF, 0.0), "sigmoid": (1.0, 0.0)}
 
 
 @pytest.mark.parametrize("name", NAMES)
@@ -117,3 +117,28 @@ def test_overflowing_preactivations(rows, override, name):
         assert bool((y[:, 1::3] == down).all()), (name, y[0, 1])
     v, bound = ma.forward(name, torch.ones(1, dtype=torch.bfloat16), torch.bfloat16)
     assert bool(((y[:, 2::3] - v).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("rows,override", [(4, None), (64, None), (256, dict(tune=128, split_c=1)),
+                                           (256, dict(tune=256, split_c=1)), (256, dict(tune=128, split_c=2))])
+@pytest.mark.parametrize("name,up,down", [("gelu", 1.0, 0.0), ("relu", 1.0, 0.0), ("sigmoid", 0.0, 0.0)])
+def test_slopes_of_overflowing_preactivations(name, up, down, rows, override):
+    """The slope at both infinities, through dwg = dg^T x with u = dy = 1."""
+    c, f = 128, 24
+    x = torch.zeros(rows, c, dtype=torch.bfloat16)
+    wg, wu = torch.zeros(f, c, dtype=torch.bfloat16), torch.zeros(f, c, dtype=torch.bfloat16)
+    x[:, 5] = 2.0 ** 100
+    x[:, 70] = 1.0
+    wg[0::2, 5] = 2.0 ** 100
+    wg[1::2, 5] = -2.0 ** 100
+    wu[:, 70] = 1.0
+    dy = torch.ones(rows, f, dtype=torch.bfloat16).cuda()
+    ops = dy, x.cuda(), wg.cuda(), wu.cuda()
+    if override is None:
+        dwg = api.gated_bwd(*ops, act=name)[1]
+    else:
+        with api.override(**override):
+            dwg = api.gated_bwd(*ops, act=name)[1]
+    dwg = dwg.double().cpu()
+    assert bool((dwg[0::2, 70] == up * rows).all()) and bool((dwg[1::2, 70] == down * rows).all()), dwg[:2, 70]
+    assert bool((dwg[0::2, 5] == up * rows * 2.0 ** 100).all()) and bool((dwg[1::2, 5] == 0).all())

@@ -40,15 +40,17 @@
 // operand's end read as zero by the view's length, columns past the
 // reduction's end by an out-of-range offset.
 //
-// Measured, bf16 normal operands: 16384 x 2048 -> 8192 forward 790 us, 1.39
-// PFLOP/s with the activation in it (the library's product of the same flops
-// alone, 8192^3, runs at 1.39); its backward pass of 8192 rows 1255 us, 1.31
-// (projections 1.17, dx 1.52, weights 1.38).  The forward and dx are bound by
+// Measured, bf16 normal operands: 16384 x 2048 -> 8192 forward 764 to 790 us by
+// card, 1.39 to 1.44 PFLOP/s with the activation in it (the library's product of
+// 8192^3 runs at 1.37 to 1.39); its backward pass of 8192 rows 1259 us, 1.31 (in
+// a trace of ten passes projections 1.12, dx 1.44, weights 1.33, while the clock
+// falls).  The forward and dx are bound by
 // power: the matrix cores are busy 73 % of the cycles and the clock falls to
 // 1.7-1.95 GHz under them (products alone, without a load, reach 2.0 PFLOP/s).
-// With a short reduction the activation counts: 50176 x 384 -> 1024 fp16 gelu 100 us,
-// 0.79 PFLOP/s, of a tile's 14.4 us 7 for its six steps and most of the others
-// for 64 activations a lane and their stores, which no products hide.
+// With a short reduction the activation counts: 50176 x 384 -> 1024 fp16 gelu 97 to
+// 105 us by card, 0.75 to 0.81 PFLOP/s, of a tile's 16 us 7 for its six steps and
+// most of the others for 64 activations a lane and their stores, which no
+// products hide.
 #include "gated.h"
 
 namespace cnhwc {
@@ -342,7 +344,14 @@ __device__ __attribute__((always_inline)) inline __amdgpu_buffer_rsrc_t view(con
 
 // dg and du stay in the caches: the next two products read them.  (The other
 // results leave with the streaming policy: kept, they crowd the operands out of
-// the L2; 16384 x 2048 -> 8192 forward 780 us instead of 752.)
+// the L2; 16384 x 2048 -> 8192 forward 783 us instead of 764 on one card, 50176 x
+// 384 -> 1024 gelu 113 instead of 109.)
+//
+// They are rounded to the operands' 16 bits, as the matrix instructions take
+// them: the gradients' relative error is 2.35e-3 in bf16 and 2.9e-4 in fp16,
+// where dg and du in fp32 leave the rounding of the result alone, 1.66e-3 and
+// 2.1e-4.  As two 16-bit terms each they would double both products, 60 % of the
+// backward pass.  The bits of a call are the same every time.
 __device__ __attribute__((always_inline)) inline void store16_at(i32x4 v, __amdgpu_buffer_rsrc_t r, uint32_t off) {
     __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
 }

@@ -187,8 +187,8 @@ struct Shape {
 // caches, and the joining launch costs 5 us.  So small tiles win where large
 // ones leave CUs idle or the reduction is short, and a reduction is split into
 // as many parts as fill the CUs.  For example 50176 x 384 -> 1024: dx on small
-// tiles 93 us, on large ones 112 us; dwg and dwu in 16 splits of the large tile
-// 99 us, unsplit on small tiles 617 us.
+// tiles 90 us, on large ones 100; dwg and dwu in 10 splits of the small tile 99 us
+// with their join, unsplit 446.
 double tile_cost(GatedProduct prod, int end, int tile, int64_t m, int64_t n, int64_t steps, int64_t s) {
     const bool big = tile == kGatedBig, dual = prod == kProj;
     const int64_t tm = ceil_div(m, tile), tn = ceil_div(n, dual ? tile / 2 : tile);
@@ -235,8 +235,8 @@ Shape choose_shape(GatedProduct prod, int end, int64_t m, int64_t n, int64_t ste
 
 // dx and the weights' gradients in one launch of small tiles, a block a tile:
 // the splits of both, if that is estimated faster than one after the other
-// (which costs a launch more, 4 us, and a second join).  3137 x 385 -> 1027: 68
-// -> 58 us for the whole backward pass.
+// (which costs a launch more, 4 us, and a second join).  3137 x 385 -> 1027: 57 us
+// for the whole backward pass, 69 one after the other.
 bool choose_pair(int64_t rows, int64_t c, int64_t fp, double apart, Shape* dx, Shape* dw) {
     const cnhwc_override& ov = current_override();
     if (ov.tune != 0 || ov.split_c != 0) return false;
@@ -286,10 +286,10 @@ GatedPlan plan_gated(const Gated& p, int op, bool x_off, bool w_off) {
     // those are masked, so only the 16-byte alignment of every row counts
     g.pack_x = x_off || p.xs % 8 != 0 || p.c % 8 != 0;
     g.pack_w = w_off || p.c % 8 != 0;
-    // The few-row kernel while x stays in registers (64 x 2048 -> 8192 20.3 us,
-    // 65 rows on tiles 22.6), up to one 16-row tile of x (16 x 4096 -> 8192 24.0
-    // us, on tiles 31; 32 rows 44) or where the tiles would need a copy of the
-    // weights first (64 x 2500 -> 1000 11.8 us, on tiles 21.5), which the
+    // The few-row kernel while x stays in registers (64 x 2048 -> 8192 21.6 us,
+    // on tiles 23.1), up to one 16-row tile of x (16 x 4096 -> 8192 25.2 us, on
+    // tiles 29.1; 32 rows 45, on tiles 30) or where the tiles would need a copy of
+    // the weights first (64 x 2500 -> 1000 12.5 us, on tiles 24.8), which the
     // backward pass makes in any case.  (By c alone, not by the pointers: the
     // workspace for any pointers has to do for aligned ones.)
     const bool bwd = op != CNHWC_OP_FWD;

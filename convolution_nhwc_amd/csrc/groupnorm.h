@@ -71,12 +71,13 @@ int launch_groupnorm_bwd(int dtype, const GnArgs& a, hipStream_t st);
 #ifdef __HIPCC__
 
 // exp2(x c), c = hi + lo: the product's rounding is made good, which the
-// hardware's exponential would scale by x.  (An infinite product has nothing to
-// make good.)
+// hardware's exponential would scale by x.  (Neither an infinite product, d inf or
+// NaN, nor an infinite result, from t = 128 on, has anything to make good: inf
+// times a negative d is -inf, and inf - inf NaN.)
 __device__ __attribute__((always_inline)) inline float exp2_of(float x, float hi, float lo) {
     const float t = x * hi, e = __builtin_amdgcn_exp2f(t);
     const float d = __builtin_fmaf(x, lo, __builtin_fmaf(x, hi, -t));
-    return __builtin_fabsf(t) < 1e4f ? __builtin_fmaf(e, d * 0.69314718056f, e) : e;
+    return t > -1e4f && t < 128.0f ? __builtin_fmaf(e, d * 0.69314718056f, e) : e;
 }
 constexpr float kLog2e = 1.44269504f, kLog2eLo = 1.92596299e-8f;   // their sum is log2(e) to 48 bits
 __device__ __attribute__((always_inline)) inline float exp_of(float x) { return exp2_of(x, kLog2e, kLog2eLo); }

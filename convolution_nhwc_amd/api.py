@@ -916,19 +916,23 @@ def _linear_operands(x, w):
     return rows, c, f, xs, ws, dt
 
 
-def linear_i8_workspace(x, w):
-    """Workspace bytes of linear_i8 for operands like x and w."""
+def linear_i8_workspace(x, w, act=None):
+    """Workspace bytes of linear_i8 for operands like x and w and this act;
+    without one, enough for every act (how a product is divided depends on it)."""
     _t()
     rows, c, f, xs, ws, dt = _linear_operands(x, w)
-    return _linear_desc(_forced.key, _off16(x, w), rows, c, f, xs, ws, 0, 0, -1, dt, BF16)[1]
+    acts = ACTS_OR_NONE.values() if act is None else (_act_or_none(act),)
+    return max(_linear_desc(_forced.key, _off16(x, w), rows, c, f, xs, ws, 0, 0, a, dt, BF16)[1] for a in acts)
 
 
-def linear_i8_plan(x, w):
+def linear_i8_plan(x, w, act="none", residual=None, y=None):
     """Names of the kernels the call runs on 16-byte-aligned operands."""
     _t()
     rows, c, f, xs, ws, dt = _linear_operands(x, w)
+    rs, ys = (_rows(t, what, f)[2] if t is not None else 0 for t, what in ((residual, "residual"), (y, "y")))
     buf = ctypes.create_string_buffer(256)
-    _check(lib().cnhwc_linear_i8_plan(ctypes.byref(LinearI8Problem(rows, c, f, xs, ws, 0, 0, -1, dt, BF16, 0)), buf, 256))
+    _check(lib().cnhwc_linear_i8_plan(ctypes.byref(LinearI8Problem(rows, c, f, xs, ws, rs, ys, _act_or_none(act), dt, BF16, 0)),
+                                      buf, 256))
     return buf.value.decode()
 
 

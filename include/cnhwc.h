@@ -477,7 +477,8 @@ typedef struct cnhwc_linear_i8_problem {
 
 /* Workspace bytes: the quantized rows and their scales, copies of operands whose
  * rows are not 16-byte aligned, partial sums of split reductions.  `unaligned`
- * != 0 sizes for any pointers. */
+ * != 0 sizes for any pointers.  (act counts: whether a reduction is split depends
+ * on what its results cost.) */
 int cnhwc_linear_i8_workspace_size(const cnhwc_linear_i8_problem* prob, int unaligned, size_t* bytes);
 
 /* Names the kernels that the call runs on 16-byte-aligned operands. */

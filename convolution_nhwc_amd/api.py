@@ -766,12 +766,17 @@ class AdamW:
     The moments of all tensors lie in flat tensors ``m`` and ``v`` (and
     ``scales`` [2, blocks] for 8 bits), tensor i's from ``offsets[i]`` on, a
     multiple of 256; ``state`` takes them as an earlier run left them, with its
-    ``steps``.  What lies between the tensors stays as it is."""
+    ``steps``, and so does assigning to ``m``, ``v`` and ``scales`` later.  What lies
+    between the tensors stays as it is.
+
+    A tensor whose memory is exchanged (``p.data = ...``, ``set_``) is followed to
+    where it lies at the next step, if its size still fits.  (A captured step keeps
+    the addresses that it was captured with.)"""
 
     def __init__(self, params, bits=32, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None, seed=0, state=None,
                  steps=0):
         torch = _t()
-        self.params = list(params)
+        self.params = tuple(params)
         if not self.params:
             raise ValueError("params is empty")
         if bits not in (8, 32):
@@ -780,61 +785,103 @@ class AdamW:
             raise ValueError("seed must be in [0, 2^64) (got %d)" % seed)
         count = len(self.params)
         decays = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
-        self.copies = list(copies) if copies is not None else [None] * count
+        self.copies = tuple(copies) if copies is not None else (None,) * count
         for what, v in (("weight_decay", decays), ("copies", self.copies)):
             if len(v) != count:
                 raise ValueError("%s has %d entries for %d tensors" % (what, len(v), count))
         self.device, self.bits, self.steps = self.params[0].device, bits, steps
-        self.offsets, at = [], 0
+        self.offsets, self._sizes, at = [], [p.numel() for p in self.params], 0
         self._list = (AdamwTensor * count)()
-        for i, (p, copy, d) in enumerate(zip(self.params, self.copies, decays)):
-            t = self._list[i]
-            t.p_dtype = self._check(p, "params[%d]" % i, p)
-            t.n, t.weight_decay = p.numel(), d
-            t.p = _ptr(p)
-            if copy is not None:
-                t.copy_dtype = self._check(copy, "copies[%d]" % i, p)
-                t.copy = _ptr(copy)
+        for t, n, d in zip(self._list, self._sizes, decays):
+            t.n, t.weight_decay = n, d
             self.offsets.append(at)
-            at += -(-t.n // ADAMW_BLOCK) * ADAMW_BLOCK
+            at += -(-n // ADAMW_BLOCK) * ADAMW_BLOCK
         kind = torch.float32 if bits == 32 else torch.uint8
+        self._shapes = [((at,), kind), ((at,), kind)] + [((2, at // ADAMW_BLOCK), torch.float32)] * (bits == 8)
         if state is None:
-            self.m = torch.zeros(at, dtype=kind, device=self.device)
-            self.v = torch.zeros_like(self.m)
-            self.scales = torch.zeros((2, at // ADAMW_BLOCK), device=self.device) if bits == 8 else None
-        else:
-            shapes = [((at,), kind), ((at,), kind)] + [((2, at // ADAMW_BLOCK), torch.float32)] * (bits == 8)
-            if len(state) != len(shapes):
-                raise ValueError("state must be (m, v%s)" % (", scales" if bits == 8 else ""))
-            for t, (shape, dtype), what in zip(state, shapes, ("m", "v", "scales")):
-                if t.device != self.device or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-                    raise ValueError("state %s must be a contiguous %s tensor of %s on %s" % (what, list(shape), dtype, self.device))
-            self.m, self.v, self.scales = (*state, None)[:3]
-        for i, o in enumerate(self.offsets):
-            t = self._list[i]
-            if t.n:
-                t.m, t.v = (s.data_ptr() + o * s.element_size() for s in (self.m, self.v))
-                if bits == 8:
-                    t.m_scale, t.v_scale = (s.data_ptr() + o // ADAMW_BLOCK * 4 for s in self.scales)
+            state = [torch.zeros(shape, dtype=dtype, device=self.device) for shape, dtype in self._shapes]
+        elif len(state) != len(self._shapes):
+            raise ValueError("state must be (m, v%s)" % (", scales" if bits == 8 else ""))
+        self._state = list(state)
+        self.grads, self._fixed, self._watched = None, [], []
+        self._look()
         self._prob = AdamwProblem(0.0, betas[0], betas[1], eps, 0, seed, bits, count)
-        self.grads = None
 
-    def _check(self, t, what, ref):
+    def _check(self, t, what, i, n):
+        fits = t.device == self.device and t.numel() == n and t.is_contiguous()
+        if fits and t.is_cuda and t.dtype in _mix_types:
+            return _mix_types[t.dtype]
+        what = "%s[%d]" % (what, i)     # (made where it is needed: it takes as long as the check)
         dt = _operand(t, what)
-        if t.device != self.device or t.numel() != ref.numel() or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous tensor of %d values on %s" % (what, ref.numel(), self.device))
+        if not fits:
+            raise ValueError("%s must be a contiguous tensor of %d values on %s" % (what, n, self.device))
         return dt
+
+    def _check_all(self, tensors, what):
+        """The element types of a list with a tensor for each of params."""
+        return [self._check(t, what, i, n) for i, (t, n) in enumerate(zip(tensors, self._sizes))]
+
+    def _look(self):
+        """Checks all tensors, then takes their addresses.  Their storages are held, so
+        that nothing else can come to lie at an address that a step compares."""
+        for t, (shape, dtype), what in zip(self._state, self._shapes, ("m", "v", "scales")):
+            if t.device != self.device or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError("state %s must be a contiguous %s tensor of %s on %s" % (what, list(shape), dtype, self.device))
+        bound = self._watched[len(self._fixed):]
+        types, grad_types = self._check_all(self.params, "params"), self._check_all(bound, "grads")
+        copy_types = [c if c is None else self._check(c, "copies", i, n) for i, (c, n) in enumerate(zip(self.copies, self._sizes))]
+        scales = self.scales if self.bits == 8 else ()
+        for t, p, dt, copy, ct, n, o in zip(self._list, self.params, types, self.copies, copy_types, self._sizes, self.offsets):
+            t.p, t.p_dtype = _ptr(p), dt
+            if copy is not None:
+                t.copy, t.copy_dtype = _ptr(copy), ct
+            if n:
+                t.m, t.v = (s.data_ptr() + o * s.element_size() for s in self._state[:2])
+                if self.bits == 8:
+                    t.m_scale, t.v_scale = (s.data_ptr() + o // ADAMW_BLOCK * 4 for s in scales)
+        self._fixed = [*self.params, *(c for c in self.copies if c is not None), *self._state]
+        self._at = [t.data_ptr() for t in self._fixed]
+        self._held = [t.untyped_storage() for t in self._fixed]
+        self._take(bound, grad_types, True)
+
+    def _take(self, grads, types, bound):
+        """Takes the addresses of checked gradients; bound: for more steps than the next."""
+        for t, g, dt in zip(self._list, grads, types):
+            t.g, t.g_dtype = _ptr(g), dt
+        later, fixed = grads if bound else [], len(self._fixed)
+        self._watched = self._fixed + later
+        self._at[fixed:] = [g.data_ptr() for g in later]
+        self._held[fixed:] = [g.untyped_storage() for g in later]
+
+    def _follow(self):
+        if list(map(_torch.Tensor.data_ptr, self._watched)) != self._at:
+            self._look()
+
+    def _exchange(self, i, what, t):
+        if i >= len(self._state) or not isinstance(t, _torch.Tensor):
+            raise ValueError("%s cannot be %s" % (what, type(t).__name__))
+        kept, self._state[i] = self._state[i], t
+        try:
+            self._look()
+        except ValueError:
+            self._state[i] = kept
+            raise
+
+    m = property(lambda self: self._state[0], lambda self, t: self._exchange(0, "m", t))
+    v = property(lambda self: self._state[1], lambda self, t: self._exchange(1, "v", t))
+    scales = property(lambda self: self._state[2] if self.bits == 8 else None, lambda self, t: self._exchange(2, "scales", t))
 
     def bind(self, grads):
         """The gradients of the steps to come: for each tensor one of its size,
         of any of the types.  A program whose gradients always lie in the same
         buffers binds them once."""
+        self._gradients(grads, True)
+
+    def _gradients(self, grads, bound):
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d tensors" % (len(grads), len(self.params)))
-        types = [self._check(g, "grads[%d]" % i, p) for i, (g, p) in enumerate(zip(grads, self.params))]
-        for t, g, dt in zip(self._list, grads, types):
-            t.g, t.g_dtype = _ptr(g), dt
+        self._take(grads, self._check_all(grads, "grads"), bound)
         self.grads = grads
 
     def step(self, lr, grads=None, grad_scale=None, device_lr=None, device_step=None):
@@ -843,15 +890,18 @@ class AdamW:
         device tensors of one value that multiply the gradients and lr, and
         device_step, an int64 one that is added to the step's number."""
         if grads is not None:
-            self.bind(grads)
-        if self.grads is None:
+            self._gradients(grads, False)
+        elif self.grads is None:
             raise ValueError("no gradients given or bound")
+        elif len(self._watched) == len(self._fixed):
+            self.bind(self.grads)     # an earlier step's
         for t, dtype, what in ((grad_scale, "float32", "grad_scale"), (device_lr, "float32", "device_lr"),
                                (device_step, "int64", "device_step")):
             if t is not None:
                 _same(t, self.m, what, getattr(_torch, dtype))
                 if t.numel() != 1:
                     raise ValueError("%s must hold one value" % what)
+        self._follow()
         q = self._prob
         q.lr, q.step = lr, self.steps + 1
         _enqueue(lib().cnhwc_adamw, self.device, ctypes.byref(q), self._list, _ptr(grad_scale), _ptr(device_lr),
@@ -861,6 +911,7 @@ class AdamW:
     def moments(self):
         """(m, v) as flat float32 tensors: what 8-bit moments stand for, or the
         fp32 moments themselves."""
+        self._follow()
         if self.bits == 32:
             return self.m, self.v
         m = _torch.empty(self.m.shape, dtype=_torch.float32, device=self.device)

@@ -761,7 +761,8 @@ class AdamW:
     updated values in its own type (the 16-bit weights of the next pass), or
     None.  bits: 32 (fp32 moments) or 8 (a byte each and a scale for every 256
     elements; see cnhwc_adamw for the codes).  weight_decay: one number, or one
-    for each tensor.  seed: of the draws that round 8-bit moments.
+    for each tensor.  seed: of the draws that round 8-bit moments (another than
+    the dropout's, which draws the same words under the same seed).
 
     The moments of all tensors lie in flat tensors ``m`` and ``v`` (and
     ``scales`` [2, blocks] for 8 bits), tensor i's from ``offsets[i]`` on, a

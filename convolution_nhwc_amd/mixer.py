@@ -87,11 +87,15 @@ class ChannelMixer:
         self.grads = {"dw": dw, "gamma": gamma, "beta": beta, "wg": wg, "wu": wu, "down": down}
         return api.dgrad(da, w["dw"], self.spatial) + dy
 
-    def adamw(self, bits=32, weight_decay=0.01, **kw):
+    def adamw(self, bits=32, weight_decay=0.01, seed=None, **kw):
         """Updates by AdamW from here on, with fp32 or 8-bit moments; the norm's
-        weights do not decay.  More arguments go to api.AdamW."""
+        weights do not decay.  The draws that round 8-bit moments come from seed (the
+        block's), by a key of their own.  More arguments go to api.AdamW."""
         fp32 = ("gamma", "beta")   # these weights are their masters
-        self.optimizer = api.AdamW([self.master[k] for k in self.NAMES], bits=bits,
+        # both draw at (element / 4, step): under one key the first tensor's moments would
+        # be rounded by the words of the dropout's mask
+        key = (self.seed if seed is None else seed) ^ 1 << 63
+        self.optimizer = api.AdamW([self.master[k] for k in self.NAMES], bits=bits, seed=key,
                                    weight_decay=[0.0 if k in fp32 else weight_decay for k in self.NAMES],
                                    copies=[None if k in fp32 else self.weights[k] for k in self.NAMES], **kw)
         return self.optimizer
@@ -147,7 +151,7 @@ def train(steps=20, n=4, h=14, w=14, c=64, f=176, dtype="bf16", rate=1.0, seed=0
     teacher = ChannelMixer(n, h, w, c, f, dtype=dtype, p=0.0, seed=seed + 1, norm=norm)
     block = ChannelMixer(n, h, w, c, f, dtype=dtype, p=0.05, seed=seed, norm=norm)
     if adamw:
-        block.adamw(adamw, seed=seed)
+        block.adamw(adamw)
     g = torch.Generator(device="cpu").manual_seed(seed + 2)
     losses = []
 

@@ -383,7 +383,8 @@ int cnhwc_groupnorm_bwd(const cnhwc_groupnorm_problem* prob, const void* dy, con
  * changes by 1 - beta of its value a step would never move.  r is drawn for
  * element i of tensor k of the list at step t: word i % 4 of Philox4x32-10 at
  * counter (i / 4 + 2^32 k, t) under the key `seed`, its low 16 bits for m and its
- * high 16 for v.  p is computed from the step's m and v before they are rounded.
+ * high 16 for v.  (For k = 0 these are cnhwc_dropout's words at offset t under the same
+ * seed: a program that draws both gives them seeds of their own.)  p is computed from the step's m and v before they are rounded.
  * A positive v keeps the least code at least, so that no step divides by eps
  * alone.  A block that holds a NaN or infinity has the scale NaN, and all its
  * elements stand for NaN.  Zero bytes with zero scales stand for 0: so moments

@@ -398,7 +398,7 @@ int launch_adamw(int bits, int deep, const AdamArgs& a, unsigned blocks, hipStre
 
 int launch_adamw_moments(int64_t n, const void* m, const void* v, const float* ms, const float* vs, float* mv,
                          float* vv, hipStream_t st) {
-    const int64_t blocks = (n + 256 * kMomentsDeep * 4 - 1) / (256 * kMomentsDeep * 4);   // (n < 2^40: under 2^28)
+    const int64_t blocks = (n + 256 * kMomentsDeep * 4 - 1) / (256 * kMomentsDeep * 4);   // (n < 2^35: at most 2^23)
     adamw_moments_kernel<<<unsigned(blocks), 256, 0, st>>>(n, m, v, ms, vs, mv, vv);
     return CNHWC_OK;
 }

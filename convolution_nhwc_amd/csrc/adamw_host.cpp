@@ -181,7 +181,8 @@ int cnhwc_adamw(const cnhwc_adamw_problem* prob, const cnhwc_adamw_tensor* tenso
 int cnhwc_adamw_moments(int64_t n, const void* m, const void* v, const float* m_scale, const float* v_scale,
                         float* m_values, float* v_values, void* hip_stream) {
     return guarded([&]() -> int {
-        if (n < 0 || n >= int64_t(1) << 40) return bad("n must be in [0, 2^40) (got " + num(n) + ")");
+        // (one launch, which has less than 2^32 threads: 16 elements each)
+        if (n < 0 || n >= int64_t(1) << 35) return bad("n must be in [0, 2^35) (got " + num(n) + ")");
         const int64_t scales = ceil_div(n, kAdamBlock) * 4;
         const View in[4] = {{"m", m, n, 1}, {"v", v, n, 1}, {"m_scale", m_scale, scales, 4}, {"v_scale", v_scale, scales, 4}};
         const View out[2] = {{"m_values", m_values, n * 4, 4}, {"v_values", v_values, n * 4, 4}};

@@ -430,7 +430,7 @@ int cnhwc_adamw(const cnhwc_adamw_problem* prob, const cnhwc_adamw_tensor* tenso
                 const float* device_lr, const int64_t* device_step, void* hip_stream);
 
 /* The fp32 values that n 8-bit moments of a tensor stand for (a scale's product
- * with its code's value, rounded once). */
+ * with its code's value, rounded once).  Valid: 0 <= n < 2^35. */
 int cnhwc_adamw_moments(int64_t n, const void* m, const void* v, const float* m_scale, const float* v_scale,
                         float* m_values, float* v_values, void* hip_stream);
 

@@ -22,9 +22,10 @@ constexpr int kGnThreads = 512;   // most threads of a block of the two-launch k
 
 // Vectors a thread of a resident kernel holds, and the most threads of its block:
 // a wave has 128 registers in a block of 1024 threads and 256 in one of 512, and
-// up to 50 (forward) or 83 hold other than x (and dy).
+// up to 50 (forward) or 83 hold other than x (and dy).  (Forward, 20 in half the threads
+// would hold less than 12.)
 // Spans that are narrower than a vector, or whose groups are, come in fewer variants.
-constexpr int kGnFwd[] = {1, 2, 4, 8, 12, 20, 32}, kGnBwd[] = {1, 2, 4, 8, 12, 16, 20};
+constexpr int kGnFwd[] = {1, 2, 4, 8, 12, 32}, kGnBwd[] = {1, 2, 4, 8, 12, 16, 20};
 constexpr bool gn_plain_only(int nv) { return nv != 4 && nv != 12; }
 constexpr int gn_fwd_threads(int nv) { return nv <= 12 ? 1024 : 512; }
 constexpr int kGnBwdThreads = 512;

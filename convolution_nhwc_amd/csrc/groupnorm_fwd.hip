@@ -301,11 +301,12 @@ __global__ __launch_bounds__(kGnThreads, 3) void gn_apply_kernel(const GnArgs a)
 template <typename T, int NV>
 void launch_nv(const GnArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)(a.n * a.s.spans));
-    const bool narrow = a.each < kVec<T>;
+    // (a span of groups of at least a vector is one too: only narrower groups' may not be whole)
     if constexpr (!gn_plain_only(NV)) {
-        if (narrow && a.s.whole) return gn_fwd_kernel<T, NV, kVec<T>, true><<<grid, a.s.threads, 0, st>>>(a);
-        if (narrow) return gn_fwd_kernel<T, NV, kVec<T>, false><<<grid, a.s.threads, 0, st>>>(a);
-        if (!a.s.whole) return gn_fwd_kernel<T, NV, 2, false><<<grid, a.s.threads, 0, st>>>(a);
+        if (a.each < kVec<T>) {
+            if (a.s.whole) return gn_fwd_kernel<T, NV, kVec<T>, true><<<grid, a.s.threads, 0, st>>>(a);
+            return gn_fwd_kernel<T, NV, kVec<T>, false><<<grid, a.s.threads, 0, st>>>(a);
+        }
     }
     gn_fwd_kernel<T, NV, 2, true><<<grid, a.s.threads, 0, st>>>(a);
 }
@@ -318,7 +319,6 @@ void launch(const GnArgs& a, hipStream_t st) {
     case 4: return launch_nv<T, 4>(a, st);
     case 8: return launch_nv<T, 8>(a, st);
     case 12: return launch_nv<T, 12>(a, st);
-    case 20: return launch_nv<T, 20>(a, st);
     case 32: return launch_nv<T, 32>(a, st);
     }
     const dim3 grid((unsigned)(a.n * a.s.spans * a.s.chunks));

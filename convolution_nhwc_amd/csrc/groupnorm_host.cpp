@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <iterator>
 #include <string>
 
 #include "groupnorm.h"
@@ -17,6 +18,7 @@ namespace cnhwc {
 // no span fits.
 static bool gn_resident(GnShape& s, int64_t v, int64_t n, int64_t pixels, int64_t each, int64_t groups, bool bwd) {
     const int* const nvs = bwd ? kGnBwd : kGnFwd;
+    const int variants = bwd ? std::size(kGnBwd) : std::size(kGnFwd);
     auto most = [&](int nv) -> int64_t { return bwd ? kGnBwdThreads : gn_fwd_threads(nv); };
     int64_t best = -1;
     for (int64_t per = 1; per <= groups; ++per) {
@@ -32,7 +34,7 @@ static bool gn_resident(GnShape& s, int64_t v, int64_t n, int64_t pixels, int64_
         if (best >= 0 && score >= best) continue;
         // few blocks: the most threads; many: four vectors a thread, so that a CU has several at work
         int nv = 0;
-        for (int i = 0; i < 7; ++i) {
+        for (int i = 0; i < variants; ++i) {
             if (!plain && gn_plain_only(nvs[i])) continue;
             const int64_t ty = ceil_div(pixels, nvs[i]);
             if (ty * vecs > most(nvs[i])) continue;

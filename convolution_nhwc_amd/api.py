@@ -927,7 +927,9 @@ class AdamW:
 def quantize_rows(x, q=None):
     """(q, scale): the rows of x [..., c] in 8-bit integers, q = x / scale to the
     nearest, and their fp32 scales [...], max|x| / 127.  A new q has rows of a
-    multiple of 16 bytes (zeros behind c), so that linear_i8 takes it as it is."""
+    multiple of 16 bytes (zeros behind c): linear_i8 takes such weights as they
+    are, and such an x too unless it has many rows of a c that is no multiple of
+    16 itself (nothing tells it of the zeros, so it makes a copy that has them)."""
     torch = _t()
     dt = _operand(x, "x")
     rows, c, xs = _rows(x, "x")

@@ -461,7 +461,8 @@ int cnhwc_quantize_rows(const cnhwc_quantize_problem* prob, const void* x, int8_
  * x [rows][c]: 8-bit integers with their x_scale [rows] (x_dtype CNHWC_I8), or values
  * (x_dtype F16, BF16 or F32; x_scale NULL), which are quantized on the way exactly as
  * cnhwc_quantize_rows does.  w [f][c] 8-bit integers (a row stride of a multiple of
- * 16 and a 16-byte-aligned base save a copy), w_scale [f]; bias [f] fp32 or NULL;
+ * 16 and a 16-byte-aligned base save a copy; of an x of 8-bit integers and more than a
+ * few rows c has to be such a multiple too), w_scale [f]; bias [f] fp32 or NULL;
  * residual [rows][f] of y's type, or NULL.  Everything after the integer sum is
  * fp32 and y is rounded once.  y may be the residual itself (same pointer and
  * stride).  Valid: 0 <= rows < 2^31; 1 <= c < 2^17; 1 <= f <= 2^20; strides 0

@@ -85,3 +85,13 @@ def test_names_follow_the_act_and_the_strides(sized):
     assert "t128" in api.linear_i8_plan(None, None, y=Rows(16384, 8192, 8195))
     assert "t128" in api.linear_i8_plan(None, None, residual=Rows(16384, 8192, 8193))
     assert "t256" in api.linear_i8_plan(None, None, residual=Rows(16384, 8192, 8200), y=Rows(16384, 8192))
+
+
+@pytest.mark.parametrize("rows,c,stride,copied", [(5000, 100, 112, True), (5000, 112, 112, False), (5000, 112, 120, True),
+                                                  (5000, 112, 128, False), (40, 100, 112, False)])
+def test_codes_that_are_copied(rows, c, stride, copied):
+    """An x of 8-bit integers goes to the tiles as it is where c and its rows are whole 16-byte units."""
+    q = api.LinearI8Problem(rows, c, 64, stride, 112, 0, 0, -1, api.I8, api.BF16, 0)
+    buf = ctypes.create_string_buffer(200)
+    assert api.lib().cnhwc_linear_i8_plan(ctypes.byref(q), buf, 200) == api.OK
+    assert ("i8_pack" in buf.value.decode()) == copied

@@ -118,14 +118,14 @@ class ChannelMixer:
 
 class ServedMixer:
     """A ChannelMixer's weights for answering: the products' rows in 8-bit
-    integers with a scale each (half the bytes that the 16-bit ones take), laid out
-    once.  The normed rows are quantized once for both projections; the residual
+    integers with a scale each (half the bytes that the 16-bit ones take), made of
+    the fp32 masters, which are rounded once so, and laid out once.  The normed rows are quantized once for both projections; the residual
     is added as the last product leaves."""
 
     def __init__(self, block):
         self.block = block
         self.dw, self.gamma, self.beta = (block.weights[k].clone() for k in ("dw", "gamma", "beta"))
-        w = block.weights
+        w = block.master
         self.products = {k: api.quantize_rows(w[k].reshape(w[k].shape[0], -1)) for k in ("wg", "wu", "down")}
 
     def forward(self, x):

@@ -854,8 +854,8 @@ class AdamW:
         self._at[fixed:] = [g.data_ptr() for g in later]
         self._held[fixed:] = [g.untyped_storage() for g in later]
 
-    def _follow(self):
-        if list(map(_torch.Tensor.data_ptr, self._watched)) != self._at:
+    def _follow(self, tensors, at):
+        if list(map(_torch.Tensor.data_ptr, tensors)) != at:
             self._look()
 
     def _exchange(self, i, what, t):
@@ -902,7 +902,7 @@ class AdamW:
                 _same(t, self.m, what, getattr(_torch, dtype))
                 if t.numel() != 1:
                     raise ValueError("%s must hold one value" % what)
-        self._follow()
+        self._follow(self._watched, self._at)
         q = self._prob
         q.lr, q.step = lr, self.steps + 1
         _enqueue(lib().cnhwc_adamw, self.device, ctypes.byref(q), self._list, _ptr(grad_scale), _ptr(device_lr),
@@ -912,7 +912,7 @@ class AdamW:
     def moments(self):
         """(m, v) as flat float32 tensors: what 8-bit moments stand for, or the
         fp32 moments themselves."""
-        self._follow()
+        self._follow(self._state, self._at[len(self._fixed) - len(self._state):len(self._fixed)])
         if self.bits == 32:
             return self.m, self.v
         m = _torch.empty(self.m.shape, dtype=_torch.float32, device=self.device)

@@ -128,16 +128,16 @@ def test_what_no_longer_fits_is_refused(steps):
         whole = t.data
         for other in (torch.zeros(299, dtype=t.dtype), torch.zeros(600, dtype=t.dtype)[::2]):
             t.data = other
-            for call in (lambda: c.opt.step(0.1), c.opt.moments):
-                with pytest.raises(ValueError, match=what):
-                    call()
+            with pytest.raises(ValueError, match=what):
+                c.opt.step(0.1)
         t.data = whole
         c.opt.step(0.1)
         assert steps[-1] == c.where()
     assert c.opt.steps == 4
     c.opt.m.data = torch.zeros(5)
-    with pytest.raises(ValueError, match="state m"):
-        c.opt.step(0.1)
+    for call in (lambda: c.opt.step(0.1), c.opt.moments):
+        with pytest.raises(ValueError, match="state m"):
+            call()
 
 
 def test_a_refused_assignment_changes_nothing(steps):

@@ -21,7 +21,7 @@
 // Integer sums are exact in any order, so split reductions give the same bits as
 // whole ones.
 //
-// 16384 x 8192 -> 8192 on large tiles: 2.85 POP/s (a library's 8192^3: 2.12).  At 2048
+// 16384 x 8192 -> 8192 on large tiles: 2.87 POP/s (a library's 8192^3: 2.1 to 2.4).  At 2048
 // channels a tile's results count: 16384 x 2048 -> 8192 takes 260 us, 320 with gelu (matrix
 // cores 42 % busy): 256 x 256 activations that no product hides.  50176 x 1024 -> 384 with
 // a residual on small tiles 43 us, 3.7 TB/s.

@@ -771,8 +771,9 @@ class AdamW:
     between the tensors stays as it is.
 
     A tensor whose memory is exchanged (``p.data = ...``, ``set_``) is followed to
-    where it lies at the next step, if its size still fits.  (A captured step keeps
-    the addresses that it was captured with.)"""
+    where it lies at the next step, if its size still fits; until then the
+    optimizer holds the memory that it had.  (A captured step keeps the addresses
+    that it was captured with.)"""
 
     def __init__(self, params, bits=32, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None, seed=0, state=None,
                  steps=0):
